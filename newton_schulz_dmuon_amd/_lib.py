@@ -43,7 +43,9 @@ EXPORTED = ("dmuon_abi_version", "dmuon_error_string", "dmuon_last_error",
             "dmuon_pack", "dmuon_unpack", "dmuon_muon_step", "dmuon_muon_step_traced",
             "dmuon_muon_step_packed", "dmuon_adamw_step", "dmuon_step_launches",
             "dmuon_nonfinite_flags_offset", "dmuon_muon_step_noalloc",
-            "dmuon_chain_status_offset")
+            "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
+            "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
+            "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad")
 
 # DMUON_NOALLOC_SCRATCH_BYTES
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -102,6 +104,21 @@ class AdamWConfig(ctypes.Structure):
     ]
 
 
+class Q8WeightDesc(ctypes.Structure):
+    """``dmuon_q8_weight``"""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("param_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("codes_t", ctypes.c_void_p),
+        ("scales_t", ctypes.c_void_p),
+    ]
+
+
 class DmuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"dmuon status {status}: {message}")
@@ -148,11 +165,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dmuon_nonfinite_flags_offset.argtypes = [P(Matrix), c_i32, P(StepConfig), P(ctypes.c_size_t)]
     lib.dmuon_chain_status_offset.argtypes = [P(Matrix), c_i32, P(StepConfig), P(ctypes.c_size_t)]
     lib.dmuon_muon_step_noalloc.argtypes = [P(Matrix), c_i32, P(StepConfig), vp]
+    size_t = ctypes.c_size_t
+    lib.dmuon_q8_quantize.argtypes = [vp, c_i32, c_i64, c_i64, vp, vp, vp]
+    lib.dmuon_q8_quantize_weights.argtypes = [P(Q8WeightDesc), c_i32, vp]
+    lib.dmuon_q8_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
+    lib.dmuon_q8_matmul.argtypes = [vp, vp, c_i64, vp, vp, c_i64, c_i64, vp, c_i32, vp, size_t, vp]
+    lib.dmuon_q8_weight_grad_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
+    lib.dmuon_q8_weight_grad.argtypes = [vp, vp, vp, c_i64, c_i64, c_i64, vp, vp, c_i32, vp, size_t,
+                                         vp]
     for name in ("dmuon_partition_lpt", "dmuon_pack_offsets", "dmuon_workspace_bytes",
                  "dmuon_pack", "dmuon_unpack", "dmuon_muon_step", "dmuon_muon_step_traced",
                  "dmuon_muon_step_packed", "dmuon_adamw_step", "dmuon_step_launches",
                  "dmuon_nonfinite_flags_offset", "dmuon_muon_step_noalloc",
-                 "dmuon_chain_status_offset"):
+                 "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
+                 "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
+                 "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.dmuon_abi_version() != ABI_VERSION:
         raise ImportError(f"libdmuon ABI {lib.dmuon_abi_version()} != {ABI_VERSION}")

@@ -17,14 +17,17 @@
 #include <vector>
 
 #include "../../include/dmuon.h"
+#include "host_common.h"
 #include "internal.h"
 
 namespace dmuon {
+
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
-int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+void clear_error() { g_last_error.clear(); }
+
 int fail(int status, const char *fmt, ...) {
   char buf[512];
   va_list ap;
@@ -35,15 +38,11 @@ int fail(int status, const char *fmt, ...) {
   return status;
 }
 
+namespace {
+
 int hip_fail(hipError_t e, const char *what) {
   return fail(DMUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
-
-int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-int64_t elem_size(int32_t dt) { return dt == DMUON_F32 ? 4 : 2; }
-
-bool dtype_ok(int32_t dt) { return dt == DMUON_BF16 || dt == DMUON_F32; }
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 constexpr int64_t kMaxNumel = int64_t(1) << 40;
@@ -52,14 +51,8 @@ constexpr int64_t kMaxNumel = int64_t(1) << 40;
 constexpr int64_t kMaxStepDim = int64_t(1) << 22;
 
 // ---------------------------------------------------------------- aliasing --
-struct Interval {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool written;
-  const char *what;
-  int32_t index;
-};
+}  // namespace
 
-// Fails if a written interval overlaps any other interval.
 int check_aliasing(std::vector<Interval> &iv) {
   std::sort(iv.begin(), iv.end(), [](const Interval &x, const Interval &y) {
     return x.lo != y.lo ? x.lo < y.lo : x.hi < y.hi;
@@ -80,7 +73,7 @@ int check_aliasing(std::vector<Interval> &iv) {
   return DMUON_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 // ------------------------------------------------------------- validation --
 int validate_config(const dmuon_step_config *cfg) {
@@ -1269,11 +1262,12 @@ int upload_static(void *dst, const std::vector<char> &src, hipStream_t st) {
   return DMUON_OK;
 }
 
+}  // namespace
+
 int check_launch(hipError_t e, const char *what) {
   return e == hipSuccess ? DMUON_OK : hip_fail(e, what);
 }
 
-}  // namespace
 }  // namespace dmuon
 
 using namespace dmuon;

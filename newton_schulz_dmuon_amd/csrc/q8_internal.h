@@ -1,0 +1,62 @@
+// Declarations shared by the 8-bit block products' entry points (q8_api.cpp)
+// and kernels (q8_quant.hip, q8_matmul.hip, q8_wgrad.hip).  Not part of the
+// C ABI.
+#pragma once
+
+#include "internal.h"
+
+namespace dmuon {
+
+// Elements that share one scale: along a row, and per side of a weight block.
+constexpr int kQ8Block = 128;
+// Range of the scale's exponent.  448 * 2^120 exceeds every finite fp32.  At
+// 2^-117 the smallest code, 2^-9, stands for 2^-126: every value that a code
+// and a scale stand for is a normal bf16 number.
+constexpr int kQ8MinExp = -117, kQ8MaxExp = 120;
+// Rows of a scale table are a multiple of this many bytes.
+constexpr int kQ8ScaleRow = 4;
+
+// Quantising weights: batches of up to kQ8Batch matrices per launch, by value.
+constexpr int kQ8Batch = 32;
+struct Q8WeightBatch {
+  int32_t n;
+  int32_t pad_;
+  int64_t first_block[kQ8Batch + 1];  // prefix sum of 128 x 128 blocks
+  const void *param[kQ8Batch];
+  uint8_t *codes[kQ8Batch], *codes_t[kQ8Batch];    // codes_t: nullable
+  uint8_t *scales[kQ8Batch], *scales_t[kQ8Batch];
+  int64_t rows[kQ8Batch], cols[kQ8Batch];
+  int32_t param_dt[kQ8Batch];
+};
+
+hipError_t launch_q8_rows(const void *x, int32_t dt, int64_t rows, int64_t cols, uint8_t *codes,
+                          uint8_t *scales, hipStream_t st);
+hipError_t launch_q8_weights(const Q8WeightBatch &b, hipStream_t st);
+
+// out[t][n] = sum over blocks b of 2^(sa[b][t] + sb[n / 128][b] - 254) *
+// sum over k in b of a[t][k] b[n][k]; all strides follow from the sizes.
+struct Q8Product {
+  const uint8_t *a, *sa;  // codes [rows][kp], scales [kp / 128][rows up to 4]
+  const uint8_t *b, *sb;  // codes [outs][kp], scales [outs up to 128 / 128][kp / 128]
+  void *out;              // [rows][outs]
+  float *ws;              // q8_matmul_workspace bytes
+  int64_t rows, outs, kp;
+  int32_t out_dt;
+};
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp);
+hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st);
+
+// out[n][k] = base[n][k] + sum over t of dy[t][n] 2^(sx[k / 128][t] - 127) x[t][k]
+struct Q8WeightGrad {
+  const void *dy;         // bf16 [rows][outs]
+  const uint8_t *x, *sx;  // codes [rows][kp], scales [kp / 128][rows up to 4]
+  const void *base;       // nullable: [outs][cols], out_dt; may be out
+  void *out;              // [outs][cols]
+  void *ws;               // q8_wgrad_workspace bytes
+  int64_t rows, outs, cols, kp;
+  int32_t out_dt;
+};
+size_t q8_wgrad_workspace(int64_t rows, int64_t outs, int64_t cols);
+hipError_t launch_q8_wgrad(const Q8WeightGrad &p, hipStream_t st);
+
+}  // namespace dmuon

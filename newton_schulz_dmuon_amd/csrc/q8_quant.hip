@@ -1,0 +1,242 @@
+// Quantisation to the 8-bit block format on gfx950: E4M3 codes and one
+// power-of-two scale 2^e per block of 128.
+//
+// e is the smallest integer with max|block| <= 448 * 2^e, clamped to
+// [kQ8MinExp, kQ8MaxExp].  448 = 1.75 * 2^8, so with max = m * 2^p (1 <= m <
+// 2) e = p - 8, or p - 7 when m > 1.75: read off the fp32 bits of the maximum,
+// with no logarithm.  A code is the value times 2^-e rounded to nearest even:
+// the product is exact in fp32 (a power of two; where it falls below fp32's
+// normal range it is far below the smallest code), so each code carries one
+// rounding.  NaN and infinities take no part in the maximum and become the
+// code NaN.
+//
+// Both kernels are one pass over the data and bound by HBM: every element is
+// read once and every code written once.
+
+#include "device_common.h"
+#include "q8_internal.h"
+
+namespace dmuon {
+
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(1))) u32x4 g_u32x4;
+typedef __attribute__((address_space(1))) u32x2 g_u32x2;
+typedef __attribute__((address_space(1))) uint32_t g_u32;
+typedef __attribute__((address_space(1))) uint8_t g_u8;
+
+constexpr int kThreads = 256;
+
+// |v| as ordered bits, 0 for NaN and infinities.
+__device__ __forceinline__ uint32_t finite_magnitude(float v) {
+  const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
+  return a < 0x7f800000u ? a : 0u;
+}
+
+// The scale byte e + 127 of a block whose largest finite magnitude has these
+// bits.
+__device__ __forceinline__ int scale_byte(uint32_t amax) {
+  const int e = static_cast<int>(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kQ8MinExp), kQ8MaxExp) + 127;
+}
+
+// 2^-e as fp32, for the scale byte e + 127 (e within the format's range, so
+// the power is a normal number).
+__device__ __forceinline__ float inverse_scale(int byte) {
+  return __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+}
+
+// A value's scaled form; infinities become NaN, which the conversion keeps.
+__device__ __forceinline__ float scaled(float v, float inv) {
+  return (__float_as_uint(v) & 0x7fffffffu) < 0x7f800000u ? v * inv : __uint_as_float(0x7fc00000u);
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(scaled(a, inv), scaled(b, inv), 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(scaled(c, inv), scaled(d, inv), r, true));
+}
+
+// Loads N consecutive elements from `i` on as fp32; `left` of them exist (the
+// rest read as zero).  vec: the address of element i is 16-byte aligned.
+template <bool F32, int N>
+__device__ __forceinline__ void load_run(const void *x, int64_t i, int64_t left, bool vec, float (&v)[N]) {
+  if (vec && left >= N) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const u32x4 r = *(const g_u32x4 *)(static_cast<const float *>(x) + i + 4 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * q + k] = __uint_as_float(r[k]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        const u32x4 r = *(const g_u32x4 *)(static_cast<const uint16_t *>(x) + i + 8 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[8 * q + 2 * k] = __uint_as_float(r[k] << 16);
+          v[8 * q + 2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = k < left ? load_elem(x, F32 ? kF32 : kBF16, i + k) : 0.f;
+  }
+}
+
+// Rows.  A wave takes 1024 columns of one row (8 blocks, 8 lanes of 16
+// elements each) and a work-group four consecutive rows, so that the four
+// scale bytes of a block's column leave as one dword of the [block][row]
+// table.  Rows behind the last are zero rows (scale byte of a zero block).
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void q8_rows_kernel(const void *__restrict__ x, int64_t rows, int64_t cols,
+                                                           int64_t kp, uint8_t *__restrict__ codes,
+                                                           uint8_t *__restrict__ scales, int64_t t4) {
+  __shared__ uint32_t bytes[4][8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 1024 + lane * 16;
+  float v[16];
+  const int64_t left = t < rows ? cols - c : 0;
+  // every row starts at a multiple of 16 bytes when the row's length is one
+  const bool vec = (cols & (F32 ? 3 : 7)) == 0;
+  load_run<F32, 16>(x, t * cols + c, left, vec, v);
+  uint32_t a = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) a = max(a, finite_magnitude(v[k]));
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), m)));
+  const int byte = scale_byte(a);
+  if (t < rows && c < kp) {
+    const float inv = inverse_scale(byte);
+    u32x4 q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = codes4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+    *(g_u32x4 *)(codes + t * kp + c) = q;
+  }
+  if ((lane & 7) == 0) bytes[wave][lane >> 3] = static_cast<uint32_t>(byte);
+  __syncthreads();
+  const int64_t kb = static_cast<int64_t>(blockIdx.y) * 8 + threadIdx.x;
+  if (threadIdx.x < 8 && kb < kp / kQ8Block) {
+    uint32_t d = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) d |= bytes[r][threadIdx.x] << (8 * r);
+    *(g_u32 *)(scales + kb * t4 + static_cast<int64_t>(blockIdx.x) * 4) = d;
+  }
+}
+
+// 4 x 4 byte transpose: r[i] holds bytes (i, 0..3); the result's word j holds
+// bytes (0..3, j).
+__device__ __forceinline__ void transpose4(const uint32_t (&r)[4], uint32_t (&o)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u);  // r0.0 r1.0 r0.1 r1.1
+  const uint32_t b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);  // r0.2 r1.2 r0.3 r1.3
+  const uint32_t c = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// Weights: one work-group per 128 x 128 block.  A thread holds an 8 x 8 patch
+// (eight 16-byte loads in flight for bf16), so that the transposed codes are a
+// byte transpose in registers and leave through LDS in whole rows.
+template <bool F32>
+__device__ __forceinline__ void q8_weight_block(const Q8WeightBatch &b, int32_t mi, int64_t blk, uint32_t *red,
+                                                char *lds) {
+  const int64_t rows = b.rows[mi], cols = b.cols[mi];
+  const int64_t nb = (rows + kQ8Block - 1) / kQ8Block, kb = (cols + kQ8Block - 1) / kQ8Block;
+  const int64_t bi = blk / kb, bj = blk % kb;
+  const int64_t kp = kb * kQ8Block, np = nb * kQ8Block;
+  const int tid = threadIdx.x;
+  const int kc = tid & 15, ng = tid >> 4;  // patch: columns 8 kc, rows 8 ng
+  const int64_t n0 = bi * kQ8Block + ng * 8, k0 = bj * kQ8Block + kc * 8;
+  const bool vec = (cols & (F32 ? 3 : 7)) == 0;
+  float v[8][8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    load_run<F32, 8>(b.param[mi], (n0 + r) * cols + k0, n0 + r < rows ? cols - k0 : 0, vec, v[r]);
+  uint32_t a = 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a = max(a, finite_magnitude(v[r][k]));
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), m)));
+  if ((tid & 63) == 0) red[tid >> 6] = a;
+  __syncthreads();
+  a = max(max(red[0], red[1]), max(red[2], red[3]));
+  const int byte = scale_byte(a);
+  const float inv = inverse_scale(byte);
+  if (tid == 0) {
+    ((g_u8 *)b.scales[mi])[bi * kb + bj] = static_cast<uint8_t>(byte);
+    if (b.scales_t[mi]) ((g_u8 *)b.scales_t[mi])[bj * nb + bi] = static_cast<uint8_t>(byte);
+  }
+  uint32_t q[8][2];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    q[r][0] = codes4(v[r][0], v[r][1], v[r][2], v[r][3], inv);
+    q[r][1] = codes4(v[r][4], v[r][5], v[r][6], v[r][7], inv);
+    if (n0 + r < rows) *(g_u32x2 *)(b.codes[mi] + (n0 + r) * kp + k0) = u32x2{q[r][0], q[r][1]};
+  }
+  if (!b.codes_t[mi]) return;
+  // LDS row k (128 bytes) holds the block's column k; its 8-byte chunk ng sits
+  // at ng ^ kc, so that the 16 lanes of a row group write distinct chunks.
+  typedef __attribute__((address_space(3))) char lds_char;
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  lds_char *const l = (lds_char *)lds;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo[4] = {q[0][h], q[1][h], q[2][h], q[3][h]}, hi[4] = {q[4][h], q[5][h], q[6][h], q[7][h]};
+    uint32_t tl[4], th[4];
+    transpose4(lo, tl);
+    transpose4(hi, th);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *(lds_u32x2 *)(l + (kc * 8 + h * 4 + j) * kQ8Block + ((ng ^ kc) * 8)) = u32x2{tl[j], th[j]};
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int k = p * 16 + (tid >> 4), chunk = tid & 15;
+    if (bj * kQ8Block + k < cols)
+      *(g_u32x2 *)(b.codes_t[mi] + (bj * kQ8Block + k) * np + bi * kQ8Block + chunk * 8) =
+          *(const lds_u32x2 *)(l + k * kQ8Block + ((chunk ^ (k >> 3)) * 8));
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void q8_weights_kernel(Q8WeightBatch b) {
+  __shared__ uint32_t red[4];
+  __shared__ __align__(16) char lds[kQ8Block * kQ8Block];
+  const int64_t w = blockIdx.x;
+  const int32_t mi = find_range(b.n, w, [&](int32_t i) { return b.first_block[i]; });
+  if (b.param_dt[mi] == kF32)
+    q8_weight_block<true>(b, mi, w - b.first_block[mi], red, lds);
+  else
+    q8_weight_block<false>(b, mi, w - b.first_block[mi], red, lds);
+}
+
+}  // namespace
+
+hipError_t launch_q8_rows(const void *x, int32_t dt, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                          hipStream_t st) {
+  const int64_t kp = (cols + kQ8Block - 1) / kQ8Block * kQ8Block;
+  const int64_t t4 = (rows + kQ8ScaleRow - 1) / kQ8ScaleRow * kQ8ScaleRow;
+  const dim3 grid(static_cast<uint32_t>(t4 / 4), static_cast<uint32_t>((kp + 1023) / 1024));
+  if (dt == kF32)
+    hipLaunchKernelGGL(q8_rows_kernel<true>, grid, dim3(kThreads), 0, st, x, rows, cols, kp, codes, scales, t4);
+  else
+    hipLaunchKernelGGL(q8_rows_kernel<false>, grid, dim3(kThreads), 0, st, x, rows, cols, kp, codes, scales, t4);
+  return hipGetLastError();
+}
+
+hipError_t launch_q8_weights(const Q8WeightBatch &b, hipStream_t st) {
+  if (b.n == 0) return hipSuccess;
+  hipLaunchKernelGGL(q8_weights_kernel, dim3(static_cast<uint32_t>(b.first_block[b.n])), dim3(kThreads), 0, st, b);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon

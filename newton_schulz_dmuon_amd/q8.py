@@ -1,0 +1,299 @@
+"""8-bit block products over torch tensors: the linear layers around the step.
+
+``q8_quantize`` turns activations (or output gradients) into 8-bit rows,
+``q8_quantize_weights`` the params into 8-bit weights, ``q8_matmul`` multiplies
+the two, forward or (``transpose=True``) for the gradient of the input, and
+``q8_weight_grad`` makes the weight gradient that ``muon_step`` reads from the
+8-bit rows the forward pass kept.  The format is described in
+``include/dmuon.h``: E4M3 codes, one power-of-two scale per block of 128.
+
+A training step of one linear layer::
+
+    w8, = nsd.q8_quantize_weights([w])
+    x8 = nsd.q8_quantize(x)                          # kept for the backward pass
+    y = nsd.q8_matmul(x8, w8)                        # x w^T
+    dx = nsd.q8_matmul(nsd.q8_quantize(dy), w8, transpose=True)   # dy w
+    nsd.q8_weight_grad(dy, x8, out=grad)             # dy^T x
+    nsd.muon_step([w], [grad], [momentum], [scale])
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import List, Optional, Sequence
+
+from . import _lib
+from ._lib import DmuonError, Q8WeightDesc, check, load
+from .api import Workspace, _dtype_code, _keep_for_stream, _ptr
+
+BLOCK = 128
+
+
+def _up(n: int, a: int) -> int:
+    return -(-n // a) * a
+
+
+class Q8Rows:
+    """8-bit rows of a ``[rows, cols]`` matrix: ``codes`` ``[rows, cols up to
+    128]`` (``torch.float8_e4m3fn``) and ``scales`` ``[cols up to 128 / 128,
+    rows up to 4]`` (``torch.uint8``, exponent + 127)."""
+
+    __slots__ = ("codes", "scales", "cols")
+
+    def __init__(self, codes, scales, cols: int):
+        self.codes, self.scales, self.cols = codes, scales, cols
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "Q8Rows":
+        import torch
+        kp = _up(cols, BLOCK)
+        return cls(torch.empty(rows, kp, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(kp // BLOCK, _up(rows, 4), dtype=torch.uint8, device=device), cols)
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+class Q8Weight:
+    """8-bit weights of a ``[rows, cols]`` matrix: ``codes`` ``[rows, cols up
+    to 128]`` and ``scales``, one per 128 x 128 block; ``codes_t`` ``[cols,
+    rows up to 128]`` and ``scales_t``, the same transposed, or None."""
+
+    __slots__ = ("codes", "scales", "codes_t", "scales_t", "rows", "cols")
+
+    def __init__(self, codes, scales, codes_t=None, scales_t=None, rows: Optional[int] = None,
+                 cols: Optional[int] = None):
+        self.codes, self.scales, self.codes_t, self.scales_t = codes, scales, codes_t, scales_t
+        self.rows = codes.shape[0] if rows is None else rows
+        # without the transposed codes the padding of cols cannot be told
+        self.cols = cols if cols is not None else \
+            (codes_t.shape[0] if codes_t is not None else codes.shape[1])
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device, transposed: bool = True) -> "Q8Weight":
+        import torch
+        np_, kp = _up(rows, BLOCK), _up(cols, BLOCK)
+        nb, kb = np_ // BLOCK, kp // BLOCK
+        f8, u8 = torch.float8_e4m3fn, torch.uint8
+        return cls(torch.empty(rows, kp, dtype=f8, device=device),
+                   torch.empty(nb, kb, dtype=u8, device=device),
+                   torch.empty(cols, np_, dtype=f8, device=device) if transposed else None,
+                   torch.empty(kb, nb, dtype=u8, device=device) if transposed else None, rows, cols)
+
+
+def _invalid(message: str) -> DmuonError:
+    return DmuonError(_lib.ERR_INVALID_ARG, message)
+
+
+def _check_tensor(t, what: str, shape, dtype, device) -> None:
+    """The checks that the C call cannot make: a kernel would read another
+    device's memory, or past the end of a smaller tensor."""
+    if t.device != device:
+        raise _invalid(f"{what} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        raise DmuonError(_lib.ERR_UNSUPPORTED_DTYPE, f"{what} has dtype {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise _invalid(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise _invalid(f"{what} must be contiguous")
+
+
+def _check_rows(q: Q8Rows, rows: int) -> None:
+    import torch
+    kp = _up(q.cols, BLOCK)
+    _check_tensor(q.codes, "codes", (rows, kp), torch.float8_e4m3fn, q.codes.device)
+    _check_tensor(q.scales, "scales", (kp // BLOCK, _up(rows, 4)), torch.uint8, q.codes.device)
+
+
+def _matrix(t, what: str):
+    """``t``'s device, rows and columns; any leading dimensions are rows."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise _invalid(f"{what} needs at least one column")
+    if not t.is_cuda:
+        raise _invalid(f"{what} is on {t.device}, not on a GPU")
+    cols = t.shape[-1]
+    return t.device, t.numel() // cols, cols
+
+
+class _On:
+    """Makes ``device`` current for the launches, as their kernels are loaded
+    per device, and gives the stream's handle."""
+
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guard = device, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.stream is not None and self.stream.device != self.device:
+            raise _invalid(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _allocated(device, stream, *tensors) -> None:
+    """Outputs and workspaces made here on the current stream and used on
+    another one are marked as in use by that stream too."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                _keep_for_stream(t, device, stream)
+
+
+def q8_quantize(x, out: Optional[Q8Rows] = None, stream=None) -> Q8Rows:
+    """8-bit rows of ``x`` (bf16 or fp32, ``[..., cols]``; the leading
+    dimensions are flattened), one scale per 1 x 128 block."""
+    device, rows, cols = _matrix(x, "x")
+    dt = _dtype_code(x)
+    if out is None:
+        out = Q8Rows.empty(rows, cols, device)
+        _allocated(device, stream, out.codes, out.scales)
+    else:
+        if out.cols != cols or out.codes.device != device:
+            raise _invalid("out does not fit x")
+        _check_rows(out, rows)
+    with _On(device, stream) as s:
+        check(load().dmuon_q8_quantize(_ptr(x), dt, rows, cols, out.codes.data_ptr(),
+                                       out.scales.data_ptr(), s))
+    return out
+
+
+def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = None,
+                        transposed: bool = True, stream=None) -> List[Q8Weight]:
+    """8-bit weights of each matrix (bf16 or fp32, ``[rows, cols]``), one scale
+    per 128 x 128 block; without ``transposed`` only what the forward product
+    reads.  All matrices lie on one device.  ``out`` takes an earlier call's
+    results, with or without their transposed codes, and overwrites them."""
+    import torch
+    n = len(params)
+    if n == 0:
+        return []
+    device = params[0].device
+    for i, p in enumerate(params):
+        if p.dim() != 2:
+            raise _invalid(f"matrix {i} is not 2-D")
+        if not p.is_cuda or p.device != device:
+            raise _invalid(f"matrix {i} is on {p.device}, not on {device} (a GPU)")
+    if out is None:
+        out = [Q8Weight.empty(p.shape[0], p.shape[1], device, transposed) for p in params]
+        for q in out:
+            _allocated(device, stream, q.codes, q.scales, q.codes_t, q.scales_t)
+    else:
+        out = list(out)
+        if len(out) != n:
+            raise _invalid(f"{len(out)} results for {n} matrices")
+        f8, u8 = torch.float8_e4m3fn, torch.uint8
+        for p, q in zip(params, out):
+            r, c = p.shape
+            np_, kp = _up(r, BLOCK), _up(c, BLOCK)
+            _check_tensor(q.codes, "codes", (r, kp), f8, device)
+            _check_tensor(q.scales, "scales", (np_ // BLOCK, kp // BLOCK), u8, device)
+            if (q.codes_t is None) != (q.scales_t is None):
+                raise _invalid("codes_t and scales_t go together")
+            if q.codes_t is not None:
+                _check_tensor(q.codes_t, "codes_t", (c, np_), f8, device)
+                _check_tensor(q.scales_t, "scales_t", (kp // BLOCK, np_ // BLOCK), u8, device)
+    arr = (Q8WeightDesc * n)()
+    for i, (p, q) in enumerate(zip(params, out)):
+        arr[i] = Q8WeightDesc(_ptr(p), _dtype_code(p), 0, p.shape[0], p.shape[1],
+                              q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.codes_t),
+                              _ptr(q.scales_t))
+    with _On(device, stream) as s:
+        check(load().dmuon_q8_quantize_weights(arr, n, s))
+    return out
+
+
+def _workspace(call, sizes, workspace: Optional[Workspace], device, stream):
+    """Device scratch for a product of these sizes: (address, bytes, tensor);
+    the tensor keeps the memory until the launches are enqueued."""
+    need = ctypes.c_size_t(0)
+    check(call(*sizes, ctypes.byref(need)))
+    if need.value == 0:
+        return None, 0, None
+    buf = (workspace or Workspace()).get(need.value, device)
+    _keep_for_stream(buf, device, stream)
+    return buf.data_ptr(), buf.numel(), buf
+
+
+def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=None,
+              workspace: Optional[Workspace] = None, stream=None):
+    """``a w^T`` (``[rows, w.rows]``) or, with ``transpose``, ``a w``
+    (``[rows, w.cols]``), bf16 (the default) or fp32: fp32 sums, one rounding.
+    ``out`` takes the result; its dtype is then the result's."""
+    import torch
+    rows, device = a.codes.shape[0], a.codes.device
+    codes, scales = (w.codes_t, w.scales_t) if transpose else (w.codes, w.scales)
+    if codes is None or scales is None:
+        raise _invalid("the weight has no transposed codes")
+    outs, inner = (w.cols, w.rows) if transpose else (w.rows, w.cols)
+    if not a.codes.is_cuda:
+        raise _invalid(f"codes are on {device}, not on a GPU")
+    if a.cols != inner:
+        raise _invalid(f"rows of {a.cols} columns against a weight of {inner}")
+    _check_rows(a, rows)
+    kp = _up(inner, BLOCK)
+    _check_tensor(codes, "the weight's codes", (outs, kp), torch.float8_e4m3fn, device)
+    _check_tensor(scales, "the weight's scales", (_up(outs, BLOCK) // BLOCK, kp // BLOCK),
+                  torch.uint8, device)
+    if out is None:
+        out = torch.empty(rows, outs, dtype=dtype or torch.bfloat16, device=device)
+        _allocated(device, stream, out)
+    else:
+        if dtype is not None and dtype != out.dtype:
+            raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
+        _check_tensor(out, "out", (rows, outs), out.dtype, device)
+    lib = load()
+    ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner), workspace,
+                               device, stream)
+    with _On(device, stream) as s:
+        check(lib.dmuon_q8_matmul(a.codes.data_ptr(), a.scales.data_ptr(), rows, codes.data_ptr(),
+                                  scales.data_ptr(), outs, inner, out.data_ptr(), _dtype_code(out),
+                                  ws, nws, s))
+    return out
+
+
+def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
+                   workspace: Optional[Workspace] = None, stream=None):
+    """``base + dy^T x`` (``[dy's columns, x.cols]``): the weight gradient of
+    ``y = x w^T`` from the bf16 gradient ``dy`` (``[..., outs]``) and the 8-bit
+    rows of ``x``.  The result is ``out`` (for instance the ``grads`` entry of
+    ``muon_step``) or a new tensor of ``dtype`` (bf16 by default, else fp32).
+    ``base`` has the result's dtype and may be ``out`` itself, which adds to
+    the gradient in place."""
+    import torch
+    device, rows, outs = _matrix(dy, "dy")
+    if dy.dtype != torch.bfloat16:
+        raise DmuonError(_lib.ERR_UNSUPPORTED_DTYPE, f"dy has dtype {dy.dtype}, not torch.bfloat16")
+    if not dy.is_contiguous():
+        raise _invalid("dy must be contiguous")
+    if x.codes.device != device:
+        raise _invalid(f"codes are on {x.codes.device}, not on {device}")
+    _check_rows(x, rows)
+    cols = x.cols
+    if out is None:
+        out = torch.empty(outs, cols, device=device,
+                          dtype=dtype or (base.dtype if base is not None else torch.bfloat16))
+        _allocated(device, stream, out)
+    else:
+        if dtype is not None and dtype != out.dtype:
+            raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
+        _check_tensor(out, "out", (outs, cols), out.dtype, device)
+    if base is not None:
+        _check_tensor(base, "base", (outs, cols), out.dtype, device)
+    lib = load()
+    ws, nws, keep = _workspace(lib.dmuon_q8_weight_grad_workspace_bytes, (rows, outs, cols),
+                               workspace, device, stream)
+    with _On(device, stream) as s:
+        check(lib.dmuon_q8_weight_grad(dy.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(), rows,
+                                       outs, cols, base.data_ptr() if base is not None else None,
+                                       out.data_ptr(), _dtype_code(out), ws, nws, s))
+    return out
