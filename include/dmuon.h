@@ -411,7 +411,8 @@ int dmuon_muon_step_noalloc(const dmuon_matrix *mats, int32_t n,
  *            cols; scales [np / 128][kp / 128], np = rows rounded up to 128;
  *            and the same codes transposed, codes_t [cols][np], zero codes
  *            behind rows, scales_t [kp / 128][np / 128]
- * Buffers: 16-byte aligned; scale tables 4-byte aligned.  Each call only
+ * Buffers: 16-byte aligned; scale tables 4-byte aligned, and read in whole
+ * 4-byte words (up to 3 bytes behind an odd-sized table).  Each call only
  * enqueues kernels and takes no host-side buffer along, so it can be captured
  * into a graph.
  */

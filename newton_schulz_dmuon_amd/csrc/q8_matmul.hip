@@ -123,11 +123,345 @@ __global__ __launch_bounds__(kWaves * 64) void q8_rows16_kernel(Q8Product p) {
   }
 }
 
+// ---- tiles: many rows ----
+//
+// One work-group of 8 waves (2 x 4) computes TS x TS outputs, TS outputs of
+// the weight by TS rows; each wave TS/2 x TS/4 in 16 x 16 blocks.  K advances
+// one 128-code block per step.  Both operand tiles go from global memory into
+// LDS by LDS-bound loads (16 bytes a lane, 128-byte rows, the 16-byte chunk
+// XORed with (row / 2) mod 8, which keeps the fragment reads off each other's
+// banks), a ring of two stages, with the step's row scales behind them.  The
+// two halves of the work-group (wm) run in ping-pong: one half's waves read
+// fragments and issue the next stage's loads while the other half's multiply,
+// switching at every barrier.
+//
+// The order of rows in LDS is free, since every lane of a load picks its
+// global row, and is chosen for the ends of the pipeline: a wave's block i,
+// row q holds output ((q % 4) * 4 + q / 4) * FM + i, so that a lane's FM
+// results of one row (FM blocks) are consecutive and its quarter-wave
+// neighbours' follow, and block j, column r of the rows' operand holds row
+// r * FN + j, so that a lane's FN scale bytes are one LDS word.
+constexpr int kTileThreads = 512;
+constexpr int kRowBytes = 128;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
+// Work-group barriers.  The memory clobbers keep the compiler from moving LDS
+// accesses across them.
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// ... once this wave's LDS reads are complete
+__device__ __forceinline__ void read_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// ... once this wave's LDS-bound loads have landed
+__device__ __forceinline__ void load_barrier() { asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Tile `w` of a launch of `total` tiles, in an order that keeps the tiles
+// running together on one XCD (work-group w runs on XCD w % 8) in bands of
+// four row tiles, which share operand panels in its L2.
+__device__ __forceinline__ void tile_of(uint32_t w, uint32_t total, uint32_t nt, uint32_t tt, uint32_t &in,
+                                        uint32_t &it) {
+  const uint32_t x = w % kXcds, q = total / kXcds, rem = total % kXcds;
+  const uint32_t idx = x * q + min(x, rem) + w / kXcds;
+  const uint32_t band = idx / (4 * nt), r = idx - band * 4 * nt;
+  const uint32_t h = min(4u, tt - band * 4);
+  in = r / h;
+  it = band * 4 + r % h;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
+
+template <int TS, bool EXACT>
+__device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p, int64_t n0, int64_t t0, int kbeg,
+                                        int kend, f32x4 (&acc)[TS / 32][TS / 64]) {
+  constexpr int FM = TS / 32, FN = TS / 64;
+  constexpr int kOperand = TS * kRowBytes, kStage = 2 * kOperand + 256;
+  constexpr int kPerLoader = TS / 64;  // 1 KB loads per wave and half of an operand tile
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const uint32_t kp = static_cast<uint32_t>(p.kp);
+  const int64_t t4 = (p.rows + 3) & ~static_cast<int64_t>(3), nkb = p.kp / kQ8Block;
+
+  const uint8_t *const gb = p.b + n0 * p.kp, *const ga = p.a + t0 * p.kp;
+  const uint8_t *const gs = p.sa + t0;
+  // the last output and row of the tile that exist, and the last scale word
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TS - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TS - 1)));
+  const uint32_t soff = static_cast<uint32_t>(min(static_cast<int64_t>(4 * (lane % (TS / 4))), t4 - 4 - t0));
+  // loads: lane l of 1 KB load j of a half fills LDS row (j * 4 + wn) * 8 + l / 8,
+  // physical chunk l % 8
+  const int q = (wn & 1) * 8 + (lane >> 3);
+  const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (((wn & 1) * 4 + (lane >> 4)) & 7)) * 16;
+  const int base_n = ((q & 3) * 4 + (q >> 2)) * FM + (wn >> 1) + wm * (TS / 2);
+  const int base_t = q * FN + (wn >> 1);
+  auto issue = [&](int slot, int kb) {
+    lds_char *const st = lds + slot * kStage;
+    const uint8_t *const bb = gb + static_cast<int64_t>(kb) * kQ8Block, *const ba = ga + static_cast<int64_t>(kb) * kQ8Block;
+    auto load = [&](const uint8_t *src, int row, int at) {
+      const uint32_t off = __umul24(static_cast<uint32_t>(row), kp) + chunk;
+      __builtin_amdgcn_global_load_lds((const void *)(src + off),
+                                       (__attribute__((address_space(3))) void *)(st + at + wn * 1024), 16, 0, 0);
+    };
+    int bn = base_n, bt = base_t;
+    // opaque: the offsets are rebuilt at every issue instead of being kept
+    // live across the loop
+    asm volatile("" : "+v"(bn), "+v"(bt));
+#pragma unroll
+    for (int j = 0; j < kPerLoader; ++j) load(bb, min(bn + 2 * j, lim_n), wm * (kOperand / 2) + j * 4096);
+    if (wm == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < kPerLoader; ++j) {
+          // row s of the tile's LDS rows: quarter s / (TS / 4), then block and column
+          const int s = h * (TS / 2) + j * 32, in_quarter = s % (TS / 4);
+          const int row = s / (TS / 4) * (TS / 4) + in_quarter / 16;
+          load(ba, min(bt + row, lim_t), kOperand + h * (kOperand / 2) + j * 4096);
+        }
+      if (wn == 0)
+        __builtin_amdgcn_global_load_lds((const void *)(gs + kb * t4 + soff),
+                                         (__attribute__((address_space(3))) void *)(st + 2 * kOperand), 4, 0, 0);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // this wave's block of the weight's scales: one byte per step
+  const int64_t nb = (n0 + wm * (TS / 2)) / kQ8Block, last_nb = (p.outs - 1) / kQ8Block;
+  const uint8_t *const sb = p.sb + min(nb, last_nb) * nkb;
+  auto weight_scale = [&](int kb) {
+    // scale tables are read in whole words (a scalar load)
+    const uintptr_t at = reinterpret_cast<uintptr_t>(sb + kb);
+    const uint32_t w = *(const __attribute__((address_space(4))) uint32_t *)(at & ~static_cast<uintptr_t>(3));
+    return static_cast<int>((w >> ((at & 3) * 8)) & 0xff);
+  };
+  auto row_scales = [&](const lds_char *st) -> uint32_t {
+    if constexpr (FN == 4) return *(const lds_u32 *)(st + 2 * kOperand + wn * 64 + r16 * 4);
+    return *(const lds_u16 *)(st + 2 * kOperand + wn * 32 + r16 * 2);
+  };
+  // 16 bytes (chunk sub * 4 + g4) of row r16 of 16-row block i of an operand;
+  // the swizzle is the same in every block
+  const uint32_t at0 = static_cast<uint32_t>(r16 * kRowBytes + ((g4 ^ (r16 >> 1)) & 7) * 16);
+  auto read = [&](const lds_char *op, int i, int sub) {
+    return *(const lds_u32x4 *)(op + (sub ? at0 ^ 64 : at0) + i * (16 * kRowBytes));
+  };
+
+  issue(kbeg & 1, kbeg);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (wm == 1) barrier();
+  for (int kb = kbeg; kb < kend; ++kb) {
+    const lds_char *const st = lds + (kb & 1) * kStage;
+    const lds_char *const opb = st + wm * (kOperand / 2), *const opa = st + kOperand + wn * (kOperand / 4);
+    // the last step loads its own block again, into the free stage, which
+    // keeps the loop free of a branch
+    issue((kb + 1) & 1, min(kb + 1, kend - 1));
+    const int wb = weight_scale(kb);
+    const uint32_t wa = row_scales(st);
+    if constexpr (!EXACT) {
+      u32x4 fb[FM][2], fa[FN][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fb[i][s] = read(opb, i, s);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fa[j][s] = read(opa, j, s);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      read_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      auto op8 = [](const u32x4 (&f)[2]) {
+        return i32x8{static_cast<int>(f[0].x), static_cast<int>(f[0].y), static_cast<int>(f[0].z),
+                     static_cast<int>(f[0].w), static_cast<int>(f[1].x), static_cast<int>(f[1].y),
+                     static_cast<int>(f[1].z), static_cast<int>(f[1].w)};
+      };
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          // the row scale's byte is an immediate of the instruction
+          if (j == 0)
+            acc[i][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op8(fb[i]), op8(fa[0]), acc[i][0], 0, 0, 0,
+                                                                         wb, 0, static_cast<int>(wa));
+          else if (j == 1)
+            acc[i][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op8(fb[i]), op8(fa[1]), acc[i][1], 0, 0, 0,
+                                                                         wb, 1, static_cast<int>(wa));
+          else if (j == 2)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op8(fb[i]), op8(fa[j]), acc[i][j], 0, 0, 0,
+                                                                         wb, 2, static_cast<int>(wa));
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op8(fb[i]), op8(fa[j]), acc[i][j], 0, 0, 0,
+                                                                         wb, 3, static_cast<int>(wa));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      // two half-steps of 64 codes, each read and multiplied in a phase of
+      // its own; the loads are waited for at the end of the second
+      const float sw = scale_of(wb);
+      float sr[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sr[j] = scale_of(static_cast<int>((wa >> (8 * j)) & 0xff));
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        u32x4 fb[FM], fa[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fb[i] = read(opb, i, s);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fa[j] = read(opa, j, s);
+        __builtin_amdgcn_sched_barrier(0);
+        read_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          bf16x8 xa[FN];
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            xa[j] = expand8(static_cast<int>(fa[j][2 * h]), static_cast<int>(fa[j][2 * h + 1]), sr[j]);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            const bf16x8 xb = expand8(static_cast<int>(fb[i][2 * h]), static_cast<int>(fb[i][2 * h + 1]), sw);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, xa[j], acc[i][j], 0, 0, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (s == 0)
+          barrier();
+        else
+          load_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (wm == 0) barrier();
+}
+
+// N consecutive outputs (4 or 8) as bf16 or fp32; vec: their address is
+// aligned to the vector.
+template <int N>
+__device__ __forceinline__ void store_run(void *out, int32_t dt, int64_t at, int64_t left, bool vec,
+                                          const float (&v)[N]) {
+  if (vec && left >= N) {
+    if (dt == kF32) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k)
+        *(g_f32x4 *)(static_cast<float *>(out) + at + 4 * k) = f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+    } else {
+      uint32_t u[N / 2];
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k)
+        u[k] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k])) |
+               (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k + 1])) << 16);
+      if constexpr (N == 8)
+        *(g_u32x4 *)(static_cast<uint16_t *>(out) + at) = u32x4{u[0], u[1], u[2], u[3]};
+      else
+        *(g_u32x2 *)(static_cast<uint16_t *>(out) + at) = u32x2{u[0], u[1]};
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < left) store_elem(out, dt, at + k, v[k]);
+  }
+}
+
+// PIECES > 1 work-groups split a tile's K blocks and write fp32 partial
+// results to the workspace, [piece][row][pitch]; a reduce launch adds them in
+// order.
+template <int TS, bool EXACT>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TS == 256 ? 2 : 4)))
+void q8_tile_kernel(Q8Product p, int32_t pieces, int64_t pitch) {
+  constexpr int FM = TS / 32, FN = TS / 64;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * (2 * TS * kRowBytes + 256)];
+  const uint32_t nt = static_cast<uint32_t>((p.outs + TS - 1) / TS), tt = static_cast<uint32_t>((p.rows + TS - 1) / TS);
+  // divisions run on the vector unit: their results are made scalar again
+  const uint32_t piece = uniform(blockIdx.x / (nt * tt));
+  uint32_t in, it;
+  tile_of(blockIdx.x - piece * nt * tt, nt * tt, nt, tt, in, it);
+  const int64_t n0 = static_cast<int64_t>(uniform(in)) * TS, t0 = static_cast<int64_t>(uniform(it)) * TS;
+  // a piece's blocks; kp / 128 <= 2^15 blocks, at most 2^10 pieces
+  const uint32_t nkb = static_cast<uint32_t>(p.kp / kQ8Block);
+  const int kbeg = static_cast<int>(uniform(nkb * piece / static_cast<uint32_t>(pieces)));
+  const int kend = static_cast<int>(uniform(nkb * (piece + 1) / static_cast<uint32_t>(pieces)));
+  f32x4 acc[FM][FN];
+  q8_tile<TS, EXACT>((lds_char *)smem, p, n0, t0, kbeg, kend, acc);
+
+  void *out = p.out;
+  int32_t dt = p.out_dt;
+  int64_t ld = p.outs;
+  if (pieces > 1) {
+    out = p.ws + static_cast<int64_t>(piece) * p.rows * pitch;
+    dt = kF32;
+    ld = pitch;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
+  const bool vec = ld % (FM == 8 && dt != kF32 ? 8 : 4) == 0;
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int64_t t = t0 + wn * (TS / 4) + r16 * FN + j;
+    if (t >= p.rows) continue;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t n = n0 + wm * (TS / 2) + (v * 4 + g4) * FM;
+      float run[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
+      store_run<FM>(out, dt, t * ld + n, p.outs - n, vec, run);
+    }
+  }
+}
+
 }  // namespace
 
-size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) { return 0; }
+namespace {
+
+// How a product runs.
+struct Plan {
+  int tile;      // 16: q8_rows16_kernel; else q8_tile_kernel's tile
+  int pieces;    // of K
+};
+
+Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
+  if (rows <= 64) return Plan{16, 1};
+  return Plan{256, 1};
+}
+
+int64_t pitch_of(int64_t outs) { return (outs + 7) & ~static_cast<int64_t>(7); }
+
+template <int TS>
+hipError_t launch_tiles(const Q8Product &p, int pieces, hipStream_t st) {
+  const int64_t tiles = ((p.outs + TS - 1) / TS) * ((p.rows + TS - 1) / TS);
+  const dim3 grid(static_cast<uint32_t>(tiles * pieces));
+  if (p.out_dt == kF32)
+    hipLaunchKernelGGL((q8_tile_kernel<TS, true>), grid, dim3(kTileThreads), 0, st, p, pieces, pitch_of(p.outs));
+  else
+    hipLaunchKernelGGL((q8_tile_kernel<TS, false>), grid, dim3(kTileThreads), 0, st, p, pieces, pitch_of(p.outs));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) {
+  const Plan pl = plan_of(rows, outs, kp);
+  if (pl.pieces == 1) return 0;
+  const size_t bytes = static_cast<size_t>(pl.pieces) * static_cast<size_t>(rows * pitch_of(outs)) * sizeof(float);
+  return (bytes + 255) & ~static_cast<size_t>(255);
+}
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
+  const Plan pl = plan_of(p.rows, p.outs, p.kp);
+  if (pl.tile == 256) return launch_tiles<256>(p, pl.pieces, st);
+  if (pl.tile == 128) return launch_tiles<128>(p, pl.pieces, st);
   const dim3 grid(static_cast<uint32_t>((p.outs + 15) / 16 * ((p.rows + 15) / 16)));
   if (p.out_dt == kF32)
     hipLaunchKernelGGL(q8_rows16_kernel<true>, grid, dim3(kWaves * 64), 0, st, p);
