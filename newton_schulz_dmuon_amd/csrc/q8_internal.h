@@ -48,12 +48,13 @@ hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st);
 
 // out[n][k] = base[n][k] + sum over t of dy[t][n] 2^(sx[k / 128][t] - 127) x[t][k]
 struct Q8WeightGrad {
-  const void *dy;         // bf16 [rows][outs]
+  const void *dy;         // bf16 [rows][outs], rows dy_ld elements apart
   const uint8_t *x, *sx;  // codes [rows][kp], scales [kp / 128][rows up to 4]
   const void *base;       // nullable: [outs][cols], out_dt; may be out
   void *out;              // [outs][cols]
   void *ws;               // q8_wgrad_workspace bytes
   int64_t rows, outs, cols, kp;
+  int64_t dy_ld;          // set by the launcher
   int32_t out_dt;
 };
 size_t q8_wgrad_workspace(int64_t rows, int64_t outs, int64_t cols);
