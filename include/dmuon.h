@@ -443,7 +443,7 @@ int dmuon_q8_quantize_weights(const dmuon_q8_weight *w, int32_t n, void *stream)
 /* Bytes of device workspace dmuon_q8_matmul needs for these sizes (0 for
  * many).  Host-only. */
 int dmuon_q8_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner,
-                                    size_t *out_bytes);
+                                    int32_t out_dtype, size_t *out_bytes);
 
 /* out[t][o] = sum_k a[t][k] * b[o][k], t < rows, o < outs, k < inner: 8-bit
  * rows (codes, scales) times 8-bit weights (codes_b, scales_b), fp32 sums,

@@ -168,7 +168,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     size_t = ctypes.c_size_t
     lib.dmuon_q8_quantize.argtypes = [vp, c_i32, c_i64, c_i64, vp, vp, vp]
     lib.dmuon_q8_quantize_weights.argtypes = [P(Q8WeightDesc), c_i32, vp]
-    lib.dmuon_q8_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
+    lib.dmuon_q8_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i32, P(size_t)]
     lib.dmuon_q8_matmul.argtypes = [vp, vp, c_i64, vp, vp, c_i64, c_i64, vp, c_i32, vp, size_t, vp]
     lib.dmuon_q8_weight_grad_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
     lib.dmuon_q8_weight_grad.argtypes = [vp, vp, vp, c_i64, c_i64, c_i64, vp, vp, c_i32, vp, size_t,

@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdmuon.so")
 SOURCES = ["host_api.cpp", "elementwise.hip", "gemm.hip", "scratch.hip", "q8_api.cpp",
-           "q8_quant.hip", "q8_matmul.hip", "q8_wgrad.hip"]
+           "q8_quant.hip", "q8_matmul.hip", "q8_wgrad.hip", "q8_reduce.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -149,12 +149,14 @@ int dmuon_q8_quantize_weights(const dmuon_q8_weight *w, int32_t n, void *stream)
   });
 }
 
-int dmuon_q8_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner, size_t *out_bytes) {
+int dmuon_q8_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner, int32_t out_dtype,
+                                    size_t *out_bytes) {
   return guarded([&]() -> int {
     if (!out_bytes) return fail(DMUON_ERR_INVALID_ARG, "out_bytes is NULL");
+    if (!dtype_ok(out_dtype)) return fail(DMUON_ERR_UNSUPPORTED_DTYPE, "dtype code %d", out_dtype);
     const int rc = check_sizes(rows, outs, inner);
     if (rc) return rc;
-    *out_bytes = q8_matmul_workspace(rows, outs, round_up(inner, kQ8Block));
+    *out_bytes = q8_matmul_workspace(rows, outs, round_up(inner, kQ8Block), out_dtype);
     return DMUON_OK;
   });
 }
@@ -174,7 +176,7 @@ int dmuon_q8_matmul(const void *codes, const void *scales, int64_t rows, const v
     if ((rc = b.add(codes_b, outs * kp, false, "codes_b"))) return rc;
     if ((rc = b.add(scales_b, round_up(outs, kQ8Block) / kQ8Block * nkb, false, "scales_b", 4))) return rc;
     if ((rc = b.add(out, rows * outs * elem_size(out_dtype), true, "out"))) return rc;
-    if ((rc = add_workspace(b, workspace, workspace_bytes, q8_matmul_workspace(rows, outs, kp)))) return rc;
+    if ((rc = add_workspace(b, workspace, workspace_bytes, q8_matmul_workspace(rows, outs, kp, out_dtype)))) return rc;
     if ((rc = b.check())) return rc;
     Q8Product p;
     p.a = static_cast<const uint8_t *>(codes);

@@ -1,5 +1,6 @@
 // Declarations shared by the 8-bit block products' entry points (q8_api.cpp)
-// and kernels (q8_quant.hip, q8_matmul.hip, q8_wgrad.hip).  Not part of the
+// and kernels (q8_quant.hip, q8_matmul.hip, q8_wgrad.hip,
+// q8_reduce.hip).  Not part of the
 // C ABI.
 #pragma once
 
@@ -33,6 +34,32 @@ hipError_t launch_q8_rows(const void *x, int32_t dt, int64_t rows, int64_t cols,
                           uint8_t *scales, hipStream_t st);
 hipError_t launch_q8_weights(const Q8WeightBatch &b, hipStream_t st);
 
+// How a product's tile x tile output tiles (na across, nb down) are shared out:
+// the first `whole` of them one work-group each, the last `tail` split into
+// `pieces` along the sum, whose fp32 results go to tile x tile slots of the
+// workspace, [tail tile][piece], and are added by a reduce launch.
+struct TileSplit {
+  uint32_t tile, na, nb;
+  uint32_t whole, tail, pieces;
+  size_t ws_bytes() const {
+    return pieces > 1 ? size_t(tail) * pieces * tile * tile * sizeof(float) : 0;
+  }
+};
+
+// What a launch of tiles costs, in microseconds, as measured (the kernels say
+// where): a step of a work-group with the chip nearly empty and full, for the
+// 256-tile (one work-group a CU) and the 128-tile (one, and two a CU).
+struct TileCosts {
+  float low256, full256, one128, two128;
+};
+// The cheapest of the splits by that measure; steps of the sum.
+TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCosts &c, float *cost = nullptr);
+
+// out[r][c] = base[r][c] (0 if null) + the sum of the pieces' results, in order,
+// rounded once to dt, over the tail tiles of a split.  base may be out.
+hipError_t launch_q8_reduce(const float *ws, const TileSplit &sp, int64_t rows, int64_t cols, const void *base,
+                            void *out, int32_t dt, hipStream_t st);
+
 // out[t][n] = sum over blocks b of 2^(sa[b][t] + sb[n / 128][b] - 254) *
 // sum over k in b of a[t][k] b[n][k]; all strides follow from the sizes.
 struct Q8Product {
@@ -43,7 +70,7 @@ struct Q8Product {
   int64_t rows, outs, kp;
   int32_t out_dt;
 };
-size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp);
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt);
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st);
 
 // out[n][k] = base[n][k] + sum over t of dy[t][n] 2^(sx[k / 128][t] - 127) x[t][k]

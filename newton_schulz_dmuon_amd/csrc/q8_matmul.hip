@@ -24,20 +24,13 @@
 // Weights b are the instruction's first operand and rows a the second: a lane
 // then holds four consecutive outputs of one row.
 
-#include "device_common.h"
-#include "q8_internal.h"
+#include "q8_device.h"
 
 namespace dmuon {
 
 namespace {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(1))) u32x4 g_u32x4;
-typedef __attribute__((address_space(1))) u32x2 g_u32x2;
-typedef __attribute__((address_space(1))) f32x4 g_f32x4;
-typedef __attribute__((address_space(1))) uint8_t g_u8;
 
 // 32 consecutive codes, one lane's share of an operand.
 __device__ __forceinline__ i32x8 load32(const uint8_t *p) {
@@ -51,7 +44,6 @@ __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float(sta
 
 // Eight codes (two dwords) times a scale as bf16, exactly.
 __device__ __forceinline__ bf16x8 expand8(int lo, int hi, float s) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
@@ -72,25 +64,6 @@ __device__ __forceinline__ f32x4 block_product(const i32x8 &b, int sb, const i32
     return acc;
   } else {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, 0, 0, 0, sb, 0, sa);
-  }
-}
-
-// Four consecutive outputs of row t, from column n on.
-__device__ __forceinline__ void store4(void *out, int32_t dt, int64_t t, int64_t n, int64_t outs, const f32x4 &v) {
-  const int64_t i = t * outs + n;
-  if (n + 4 <= outs && (outs & 3) == 0) {
-    if (dt == kF32) {
-      *(g_f32x4 *)(static_cast<float *>(out) + i) = v;
-    } else {
-      u32x2 u;
-      u.x = static_cast<uint32_t>(f32_to_bf16_bits(v[0])) | (static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16);
-      u.y = static_cast<uint32_t>(f32_to_bf16_bits(v[2])) | (static_cast<uint32_t>(f32_to_bf16_bits(v[3])) << 16);
-      *(g_u32x2 *)(static_cast<uint16_t *>(out) + i) = u;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (n + k < outs) store_elem(out, dt, i + k, v[k]);
   }
 }
 
@@ -119,7 +92,11 @@ __global__ __launch_bounds__(kWaves * 64) void q8_rows16_kernel(Q8Product p) {
   if (wave == 0) {
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
-    if (t0 + r16 < p.rows) store4(p.out, p.out_dt, t0 + r16, n0 + 4 * g4, p.outs, acc);
+    if (t0 + r16 < p.rows) {
+      float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+      const int64_t n = n0 + 4 * g4;
+      finish_run<4>(nullptr, p.out, p.out_dt, (t0 + r16) * p.outs + n, p.outs - n, p.outs % 4 == 0, v);
+    }
   }
 }
 
@@ -143,35 +120,6 @@ __global__ __launch_bounds__(kWaves * 64) void q8_rows16_kernel(Q8Product p) {
 // r * FN + j, so that a lane's FN scale bytes are one LDS word.
 constexpr int kTileThreads = 512;
 constexpr int kRowBytes = 128;
-typedef __attribute__((address_space(3))) char lds_char;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) uint32_t lds_u32;
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
-
-// Work-group barriers.  The memory clobbers keep the compiler from moving LDS
-// accesses across them.
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
-// ... once this wave's LDS reads are complete
-__device__ __forceinline__ void read_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-// ... once this wave's LDS-bound loads have landed
-__device__ __forceinline__ void load_barrier() { asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// Tile `w` of a launch of `total` tiles, in an order that keeps the tiles
-// running together on one XCD (work-group w runs on XCD w % 8) in bands of
-// four row tiles, which share operand panels in its L2.
-__device__ __forceinline__ void tile_of(uint32_t w, uint32_t total, uint32_t nt, uint32_t tt, uint32_t &in,
-                                        uint32_t &it) {
-  const uint32_t x = w % kXcds, q = total / kXcds, rem = total % kXcds;
-  const uint32_t idx = x * q + min(x, rem) + w / kXcds;
-  const uint32_t band = idx / (4 * nt), r = idx - band * 4 * nt;
-  const uint32_t h = min(4u, tt - band * 4);
-  in = r / h;
-  it = band * 4 + r % h;
-}
-
-__device__ __forceinline__ uint32_t uniform(uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
-}
 
 template <int TS, bool EXACT>
 __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p, int64_t n0, int64_t t0, int kbeg,
@@ -274,7 +222,7 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
         for (int j = 0; j < FN; ++j) fa[j][s] = read(opa, j, s);
       }
       __builtin_amdgcn_sched_barrier(0);
-      read_barrier();
+      lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
       auto op8 = [](const u32x4 (&f)[2]) {
         return i32x8{static_cast<int>(f[0].x), static_cast<int>(f[0].y), static_cast<int>(f[0].z),
@@ -318,7 +266,7 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
 #pragma unroll
         for (int j = 0; j < FN; ++j) fa[j] = read(opa, j, s);
         __builtin_amdgcn_sched_barrier(0);
-        read_barrier();
+        lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -346,77 +294,31 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
   if (wm == 0) barrier();
 }
 
-// N consecutive outputs (4 or 8) as bf16 or fp32; vec: their address is
-// aligned to the vector.
-template <int N>
-__device__ __forceinline__ void store_run(void *out, int32_t dt, int64_t at, int64_t left, bool vec,
-                                          const float (&v)[N]) {
-  if (vec && left >= N) {
-    if (dt == kF32) {
-#pragma unroll
-      for (int k = 0; k < N / 4; ++k)
-        *(g_f32x4 *)(static_cast<float *>(out) + at + 4 * k) = f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
-    } else {
-      uint32_t u[N / 2];
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k)
-        u[k] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k])) |
-               (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k + 1])) << 16);
-      if constexpr (N == 8)
-        *(g_u32x4 *)(static_cast<uint16_t *>(out) + at) = u32x4{u[0], u[1], u[2], u[3]};
-      else
-        *(g_u32x2 *)(static_cast<uint16_t *>(out) + at) = u32x2{u[0], u[1]};
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (k < left) store_elem(out, dt, at + k, v[k]);
-  }
-}
-
-// PIECES > 1 work-groups split a tile's K blocks and write fp32 partial
-// results to the workspace, [piece][row][pitch]; a reduce launch adds them in
-// order.
 template <int TS, bool EXACT>
 __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TS == 256 ? 2 : 4)))
-void q8_tile_kernel(Q8Product p, int32_t pieces, int64_t pitch) {
+void q8_tile_kernel(Q8Product p, TileSplit sp) {
   constexpr int FM = TS / 32, FN = TS / 64;
   __shared__ __attribute__((aligned(1024))) char smem[2 * (2 * TS * kRowBytes + 256)];
-  const uint32_t nt = static_cast<uint32_t>((p.outs + TS - 1) / TS), tt = static_cast<uint32_t>((p.rows + TS - 1) / TS);
-  // divisions run on the vector unit: their results are made scalar again
-  const uint32_t piece = uniform(blockIdx.x / (nt * tt));
-  uint32_t in, it;
-  tile_of(blockIdx.x - piece * nt * tt, nt * tt, nt, tt, in, it);
-  const int64_t n0 = static_cast<int64_t>(uniform(in)) * TS, t0 = static_cast<int64_t>(uniform(it)) * TS;
-  // a piece's blocks; kp / 128 <= 2^15 blocks, at most 2^10 pieces
-  const uint32_t nkb = static_cast<uint32_t>(p.kp / kQ8Block);
-  const int kbeg = static_cast<int>(uniform(nkb * piece / static_cast<uint32_t>(pieces)));
-  const int kend = static_cast<int>(uniform(nkb * (piece + 1) / static_cast<uint32_t>(pieces)));
+  const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ8Block));
+  const int64_t n0 = static_cast<int64_t>(w.a) * TS, t0 = static_cast<int64_t>(w.b) * TS;
   f32x4 acc[FM][FN];
-  q8_tile<TS, EXACT>((lds_char *)smem, p, n0, t0, kbeg, kend, acc);
+  q8_tile<TS, EXACT>((lds_char *)smem, p, n0, t0, w.begin, w.end, acc);
 
-  void *out = p.out;
-  int32_t dt = p.out_dt;
-  int64_t ld = p.outs;
-  if (pieces > 1) {
-    out = p.ws + static_cast<int64_t>(piece) * p.rows * pitch;
-    dt = kF32;
-    ld = pitch;
-  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
-  const bool vec = ld % (FM == 8 && dt != kF32 ? 8 : 4) == 0;
+  const TileOut o = tile_out(w, TS, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
+  const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int64_t t = t0 + wn * (TS / 4) + r16 * FN + j;
-    if (t >= p.rows) continue;
+    const int r = wn * (TS / 4) + r16 * FN + j;
+    if (r >= o.rows) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int64_t n = n0 + wm * (TS / 2) + (v * 4 + g4) * FM;
+      const int c = wm * (TS / 2) + (v * 4 + g4) * FM;
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
-      store_run<FM>(out, dt, t * ld + n, p.outs - n, vec, run);
+      finish_run<FM>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, vec, run);
     }
   }
 }
@@ -425,43 +327,49 @@ void q8_tile_kernel(Q8Product p, int32_t pieces, int64_t pitch) {
 
 namespace {
 
-// How a product runs.
+// Microseconds a step of one K block, measured on 80 .. 4096 rows: bf16, 1.03
+// with one work-group on the chip and 1.5 with 256 (the clock gives way), a
+// 128-tile 0.6 alone on its CU and 1.06 for two; fp32 results 2.23 and 2.9,
+// 0.94 and 1.88.
+constexpr TileCosts kBf16Costs = {1.03f, 1.5f, 0.6f, 1.06f}, kExactCosts = {2.23f, 2.9f, 0.95f, 1.88f};
+
+// How a product runs: 16-row kernel or tiles.
 struct Plan {
-  int tile;      // 16: q8_rows16_kernel; else q8_tile_kernel's tile
-  int pieces;    // of K
+  bool tiles;
+  TileSplit split;
 };
 
-Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
-  if (rows <= 64) return Plan{16, 1};
-  return Plan{256, 1};
+Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
+  Plan pl{};
+  if (rows <= 64) return pl;
+  pl.tiles = true;
+  pl.split = choose_split(outs, rows, kp / kQ8Block, out_dt == kF32 ? kExactCosts : kBf16Costs);
+  return pl;
 }
 
-int64_t pitch_of(int64_t outs) { return (outs + 7) & ~static_cast<int64_t>(7); }
-
 template <int TS>
-hipError_t launch_tiles(const Q8Product &p, int pieces, hipStream_t st) {
-  const int64_t tiles = ((p.outs + TS - 1) / TS) * ((p.rows + TS - 1) / TS);
-  const dim3 grid(static_cast<uint32_t>(tiles * pieces));
+hipError_t launch_tiles(const Q8Product &p, const TileSplit &sp, hipStream_t st) {
+  const dim3 grid(sp.whole + sp.tail * sp.pieces);
   if (p.out_dt == kF32)
-    hipLaunchKernelGGL((q8_tile_kernel<TS, true>), grid, dim3(kTileThreads), 0, st, p, pieces, pitch_of(p.outs));
+    hipLaunchKernelGGL((q8_tile_kernel<TS, true>), grid, dim3(kTileThreads), 0, st, p, sp);
   else
-    hipLaunchKernelGGL((q8_tile_kernel<TS, false>), grid, dim3(kTileThreads), 0, st, p, pieces, pitch_of(p.outs));
+    hipLaunchKernelGGL((q8_tile_kernel<TS, false>), grid, dim3(kTileThreads), 0, st, p, sp);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) {
-  const Plan pl = plan_of(rows, outs, kp);
-  if (pl.pieces == 1) return 0;
-  const size_t bytes = static_cast<size_t>(pl.pieces) * static_cast<size_t>(rows * pitch_of(outs)) * sizeof(float);
-  return (bytes + 255) & ~static_cast<size_t>(255);
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
+  return plan_of(rows, outs, kp, out_dt).split.ws_bytes();
 }
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
-  const Plan pl = plan_of(p.rows, p.outs, p.kp);
-  if (pl.tile == 256) return launch_tiles<256>(p, pl.pieces, st);
-  if (pl.tile == 128) return launch_tiles<128>(p, pl.pieces, st);
+  const Plan pl = plan_of(p.rows, p.outs, p.kp, p.out_dt);
+  if (pl.tiles) {
+    const hipError_t e = pl.split.tile == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
+    if (e != hipSuccess || pl.split.pieces == 1) return e;
+    return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
+  }
   const dim3 grid(static_cast<uint32_t>((p.outs + 15) / 16 * ((p.rows + 15) / 16)));
   if (p.out_dt == kF32)
     hipLaunchKernelGGL(q8_rows16_kernel<true>, grid, dim3(kWaves * 64), 0, st, p);

@@ -13,19 +13,11 @@
 // Both kernels are one pass over the data and bound by HBM: every element is
 // read once and every code written once.
 
-#include "device_common.h"
-#include "q8_internal.h"
+#include "q8_device.h"
 
 namespace dmuon {
 
 namespace {
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(1))) u32x4 g_u32x4;
-typedef __attribute__((address_space(1))) u32x2 g_u32x2;
-typedef __attribute__((address_space(1))) uint32_t g_u32;
-typedef __attribute__((address_space(1))) uint8_t g_u8;
 
 constexpr int kThreads = 256;
 
@@ -185,8 +177,6 @@ __device__ __forceinline__ void q8_weight_block(const Q8WeightBatch &b, int32_t 
   if (!b.codes_t[mi]) return;
   // LDS row k (128 bytes) holds the block's column k; its 8-byte chunk ng sits
   // at ng ^ kc, so that the 16 lanes of a row group write distinct chunks.
-  typedef __attribute__((address_space(3))) char lds_char;
-  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
   lds_char *const l = (lds_char *)lds;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -252,12 +252,12 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
         _check_tensor(out, "out", (rows, outs), out.dtype, device)
     lib = load()
-    ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner), workspace,
-                               device, stream)
+    dt = _dtype_code(out)
+    ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner, dt),
+                               workspace, device, stream)
     with _On(device, stream) as s:
         check(lib.dmuon_q8_matmul(a.codes.data_ptr(), a.scales.data_ptr(), rows, codes.data_ptr(),
-                                  scales.data_ptr(), outs, inner, out.data_ptr(), _dtype_code(out),
-                                  ws, nws, s))
+                                  scales.data_ptr(), outs, inner, out.data_ptr(), dt, ws, nws, s))
     return out
 
 

@@ -102,18 +102,22 @@ def test_weight_grad_refusals(lib, kw, want):
     assert wgrad(lib, **kw) == want
 
 
-@pytest.mark.parametrize("call", ["dmuon_q8_matmul_workspace_bytes", "dmuon_q8_weight_grad_workspace_bytes"])
-def test_workspace_bytes(lib, call):
+@pytest.mark.parametrize("call,extra", [("dmuon_q8_matmul_workspace_bytes", (_lib.BF16,)),
+                                        ("dmuon_q8_matmul_workspace_bytes", (_lib.F32,)),
+                                        ("dmuon_q8_weight_grad_workspace_bytes", ())])
+def test_workspace_bytes(lib, call, extra):
     fn = getattr(lib, call)
     out = ctypes.c_size_t(7)
-    assert fn(16, 256, 256, None) == _lib.ERR_INVALID_ARG
-    assert fn(-1, 256, 256, ctypes.byref(out)) == _lib.ERR_INVALID_ARG
-    assert fn(16, 0, 256, ctypes.byref(out)) == _lib.ERR_INVALID_ARG
-    assert fn(16, 256, 0, ctypes.byref(out)) == _lib.ERR_INVALID_ARG
+    ref = ctypes.byref(out)
+    assert fn(16, 256, 256, *extra, None) == _lib.ERR_INVALID_ARG
+    assert fn(-1, 256, 256, *extra, ref) == _lib.ERR_INVALID_ARG
+    assert fn(16, 0, 256, *extra, ref) == _lib.ERR_INVALID_ARG
+    assert fn(16, 256, 0, *extra, ref) == _lib.ERR_INVALID_ARG
     for t in (0, 1, 16, 17, 100, 1000, 8192, 100_000):
         for n, k in ((1, 1), (128, 128), (1024, 4096), (14336, 4096), (1001, 513)):
-            assert fn(t, n, k, ctypes.byref(out)) == _lib.OK
-            assert out.value % 256 == 0 and out.value < 1 << 33
+            assert fn(t, n, k, *extra, ref) == _lib.OK
+            # at most 16 pieces of fewer tiles than fill the chip, and a padded dy
+            assert out.value % 256 == 0 and out.value <= (16 * 512 * 128 * 128 * 4) + 2 * t * (n + 263)
 
 
 def status(fn, *a, **kw):
