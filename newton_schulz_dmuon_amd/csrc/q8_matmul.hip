@@ -24,6 +24,8 @@
 // Weights b are the instruction's first operand and rows a the second: a lane
 // then holds four consecutive outputs of one row.
 
+#include <algorithm>
+
 #include "q8_device.h"
 
 namespace dmuon {
@@ -32,9 +34,10 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// 32 consecutive codes, one lane's share of an operand.
+// One lane's share of a row's block: 16 codes of each half of the block, so
+// that the four lanes of a row read 64 consecutive bytes at a time.
 __device__ __forceinline__ i32x8 load32(const uint8_t *p) {
-  const u32x4 lo = *(const g_u32x4 *)p, hi = *(const g_u32x4 *)(p + 16);
+  const u32x4 lo = *(const g_u32x4 *)p, hi = *(const g_u32x4 *)(p + 64);
   return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
                static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
 }
@@ -67,36 +70,105 @@ __device__ __forceinline__ f32x4 block_product(const i32x8 &b, int sb, const i32
   }
 }
 
-// 16 outputs x 16 rows per work-group; its waves split the K blocks and add
-// their sums through LDS in wave order.  Rows and outputs behind the last are
-// clamped for the loads and not stored.
-constexpr int kWaves = 4;
-template <bool EXACT>
-__global__ __launch_bounds__(kWaves * 64) void q8_rows16_kernel(Q8Product p) {
-  __shared__ f32x4 part[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// A scale byte of a weight block, the same in every lane: scale tables are
+// read in whole words (a scalar load).
+__device__ __forceinline__ int uniform_scale(const uint8_t *p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t w = *(const __attribute__((address_space(4))) uint32_t *)(at & ~static_cast<uintptr_t>(3));
+  return static_cast<int>((w >> ((at & 3) * 8)) & 0xff);
+}
+
+// ---- few rows: the weight's bytes ----
+//
+// A work-group takes 16 NN outputs of up to 16 NT rows, its WAVES waves every
+// WAVES-th K block: together they stream whole runs of the weight's rows, each
+// byte of which is read once, straight into registers (no other wave wants it).
+// The rows' codes come from L2, once per 16 NN outputs.  Each wave keeps kAhead
+// blocks' loads in flight; the waves' sums are added through LDS in wave order.
+// Rows and outputs behind the last are clamped for the loads and not stored.
+// Column r of row block j is row r * NT + j, so that a lane's NT scale bytes
+// are one load.
+template <int NT, int NN, int WAVES, bool EXACT>
+__global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
+  constexpr int kAhead = NT * NN > 2 ? 2 : 4;
+  __shared__ f32x4 part[WAVES][NT * NN][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const uint32_t nt = static_cast<uint32_t>((p.outs + 15) / 16);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x % nt) * 16, t0 = static_cast<int64_t>(blockIdx.x / nt) * 16;
-  const int64_t n = min(n0 + r16, p.outs - 1), t = min(t0 + r16, p.rows - 1);
-  const int64_t nkb = p.kp / kQ8Block, t4 = (p.rows + 3) & ~static_cast<int64_t>(3);
-  const uint8_t *b = p.b + n * p.kp + g4 * 32, *a = p.a + t * p.kp + g4 * 32;
-  const uint8_t *sb = p.sb + (n0 / kQ8Block) * nkb;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t kb = wave; kb < nkb; kb += kWaves) {
-    const int wb = ((const g_u8 *)sb)[kb], wa = ((const g_u8 *)p.sa)[kb * t4 + t];
-    acc = block_product<EXACT>(load32(b + kb * kQ8Block), wb, load32(a + kb * kQ8Block), wa, acc);
-  }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave == 0) {
+  const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * (16 * NT);
+  const int nkb = static_cast<int>(p.kp / kQ8Block);
+  const int64_t t4 = (p.rows + 3) & ~static_cast<int64_t>(3);
+  const uint8_t *a[NT], *b[NN];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) acc += part[w][lane];
-    if (t0 + r16 < p.rows) {
-      float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-      const int64_t n = n0 + 4 * g4;
-      finish_run<4>(nullptr, p.out, p.out_dt, (t0 + r16) * p.outs + n, p.outs - n, p.outs % 4 == 0, v);
+  for (int i = 0; i < NN; ++i) b[i] = p.b + min(n0 + i * 16 + r16, p.outs - 1) * p.kp + g4 * 16;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) a[j] = p.a + min(t0 + r16 * NT + j, p.rows - 1) * p.kp + g4 * 16;
+  const uint8_t *const sa = p.sa + min(t0 + r16 * NT, t4 - NT);
+  const uint8_t *const sb = p.sb + n0 / kQ8Block * nkb;  // 16 NN divides 128
+  f32x4 acc[NN][NT];
+#pragma unroll
+  for (int i = 0; i < NN; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  i32x8 fb[kAhead][NN], fa[kAhead][NT];
+  uint32_t wa[kAhead];
+  int wb[kAhead];
+  auto load = [&](int u, int block) {
+    const int kb = min(block, nkb - 1);
+#pragma unroll
+    for (int i = 0; i < NN; ++i) fb[u][i] = load32(b[i] + static_cast<int64_t>(kb) * kQ8Block);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fa[u][j] = load32(a[j] + static_cast<int64_t>(kb) * kQ8Block);
+    const uint8_t *const s = sa + kb * t4;
+    if constexpr (NT == 4)
+      wa[u] = *(const g_u32 *)s;
+    else if constexpr (NT == 2)
+      wa[u] = *(const g_u16 *)s;
+    else
+      wa[u] = *(const g_u8 *)s;
+    wb[u] = uniform_scale(sb + kb);
+  };
+  auto multiply = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        acc[i][j] =
+            block_product<EXACT>(fb[u][i], wb[u], fa[u][j], static_cast<int>((wa[u] >> (8 * j)) & 0xff), acc[i][j]);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, wave + u * WAVES);
+  // each block's registers take the block kAhead further on as soon as it has
+  // been multiplied; the last kAhead blocks load nothing more
+  int k0 = wave;
+  for (; k0 + WAVES * kAhead < nkb; k0 += WAVES * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      multiply(u);
+      load(u, k0 + (kAhead + u) * WAVES);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (k0 + u * WAVES < nkb) multiply(u);
+#pragma unroll
+  for (int i = 0; i < NN; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < (NN * NT + WAVES - 1) / WAVES; ++q) {
+    const int at = q * WAVES + wave;
+    if (at >= NN * NT) return;
+    f32x4 sum = part[0][at][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) sum += part[w][at][lane];
+    const int64_t t = t0 + r16 * NT + at % NT, n = n0 + at / NT * 16 + 4 * g4;
+    if (t >= p.rows) continue;
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, p.outs % 4 == 0, v);
   }
 }
 
@@ -184,12 +256,6 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
   // this wave's block of the weight's scales: one byte per step
   const int64_t nb = (n0 + wm * (TS / 2)) / kQ8Block, last_nb = (p.outs - 1) / kQ8Block;
   const uint8_t *const sb = p.sb + min(nb, last_nb) * nkb;
-  auto weight_scale = [&](int kb) {
-    // scale tables are read in whole words (a scalar load)
-    const uintptr_t at = reinterpret_cast<uintptr_t>(sb + kb);
-    const uint32_t w = *(const __attribute__((address_space(4))) uint32_t *)(at & ~static_cast<uintptr_t>(3));
-    return static_cast<int>((w >> ((at & 3) * 8)) & 0xff);
-  };
   auto row_scales = [&](const lds_char *st) -> uint32_t {
     if constexpr (FN == 4) return *(const lds_u32 *)(st + 2 * kOperand + wn * 64 + r16 * 4);
     return *(const lds_u16 *)(st + 2 * kOperand + wn * 32 + r16 * 2);
@@ -210,7 +276,7 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
     // the last step loads its own block again, into the free stage, which
     // keeps the loop free of a branch
     issue((kb + 1) & 1, min(kb + 1, kend - 1));
-    const int wb = weight_scale(kb);
+    const int wb = uniform_scale(sb + kb);
     const uint32_t wa = row_scales(st);
     if constexpr (!EXACT) {
       u32x4 fb[FM][2], fa[FN][2];
@@ -333,17 +399,50 @@ namespace {
 // 0.94 and 1.88.
 constexpr TileCosts kBf16Costs = {1.03f, 1.5f, 0.6f, 1.06f}, kExactCosts = {2.23f, 2.9f, 0.95f, 1.88f};
 
-// How a product runs: 16-row kernel or tiles.
+// How a product runs: streamed (row blocks and waves of a work-group) or in
+// tiles.
 struct Plan {
-  bool tiles;
+  int nt, nn, waves;  // nt = 0: tiles
   TileSplit split;
 };
 
+// The streaming kernel's time in microseconds, as measured (rows 1 .. 128 of
+// weights 1024 x 4096 to 18944 x 3584, within 15%): a work-group takes in its
+// weight and row codes at 33 GB/s, 256 of them at a time, or the weight comes
+// from memory at 4.9 TB/s, whichever is longer.  64 rows of a 14336 x 4096
+// weight: 26 us with 4 x 2 blocks a work-group, 54 with one; of a 1024 x 4096
+// weight: 14 and 6.1.
+float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
+  const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
+  const float bytes = static_cast<float>((16 * nn + std::min<int64_t>(16 * nt, rows)) * kp);
+  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 33e3f;
+  return 3.f + std::max(taken, static_cast<float>(outs * kp) / 4.9e6f);
+}
+// Rows up to which it is considered: 512 rows of a 256 x 1536 weight still take
+// 4.8 us against 10.0 in tiles, of a 1024 x 4096 one 14.5 against 16.7.
+constexpr int64_t kStreamRows = 1024;
+
 Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
   Plan pl{};
-  if (rows <= 64) return pl;
-  pl.tiles = true;
-  pl.split = choose_split(outs, rows, kp / kQ8Block, out_dt == kF32 ? kExactCosts : kBf16Costs);
+  if (rows == 0) return pl;
+  float us;
+  pl.split = choose_split(outs, rows, kp / kQ8Block, out_dt == kF32 ? kExactCosts : kBf16Costs, &us);
+  if (rows > kStreamRows) return pl;
+  for (const int nt : {1, 2, 4})
+    for (const int nn : {1, 2}) {
+      const float s = stream_us(rows, outs, kp, nt, nn);
+      if (s >= us) continue;
+      us = s;
+      pl.nt = nt;
+      pl.nn = nn;
+    }
+  // Eight waves share K where it is long and a work-group has one row block
+  // (one row, 4096 x 4096: 5.7 us against 6.2 with four), else four (24 rows,
+  // 4096 x 14336: 20.5 against 22.1; 16 rows, 256 x 1536: 3.8 against 5.5).
+  if (pl.nt) {
+    pl.waves = pl.nt == 1 && kp >= 32 * kQ8Block ? 8 : 4;
+    pl.split = TileSplit{};
+  }
   return pl;
 }
 
@@ -357,6 +456,22 @@ hipError_t launch_tiles(const Q8Product &p, const TileSplit &sp, hipStream_t st)
   return hipGetLastError();
 }
 
+template <int NT, int NN, int WAVES>
+hipError_t launch_stream(const Q8Product &p, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN) * ((p.rows + 16 * NT - 1) / (16 * NT))));
+  if (p.out_dt == kF32)
+    hipLaunchKernelGGL((q8_stream_kernel<NT, NN, WAVES, true>), grid, dim3(WAVES * 64), 0, st, p);
+  else
+    hipLaunchKernelGGL((q8_stream_kernel<NT, NN, WAVES, false>), grid, dim3(WAVES * 64), 0, st, p);
+  return hipGetLastError();
+}
+
+template <int NT>
+hipError_t launch_stream(const Q8Product &p, int nn, int waves, hipStream_t st) {
+  if (nn == 2) return waves == 4 ? launch_stream<NT, 2, 4>(p, st) : launch_stream<NT, 2, 8>(p, st);
+  return waves == 4 ? launch_stream<NT, 1, 4>(p, st) : launch_stream<NT, 1, 8>(p, st);
+}
+
 }  // namespace
 
 size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
@@ -365,17 +480,12 @@ size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_d
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
   const Plan pl = plan_of(p.rows, p.outs, p.kp, p.out_dt);
-  if (pl.tiles) {
-    const hipError_t e = pl.split.tile == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
-    if (e != hipSuccess || pl.split.pieces == 1) return e;
-    return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
-  }
-  const dim3 grid(static_cast<uint32_t>((p.outs + 15) / 16 * ((p.rows + 15) / 16)));
-  if (p.out_dt == kF32)
-    hipLaunchKernelGGL(q8_rows16_kernel<true>, grid, dim3(kWaves * 64), 0, st, p);
-  else
-    hipLaunchKernelGGL(q8_rows16_kernel<false>, grid, dim3(kWaves * 64), 0, st, p);
-  return hipGetLastError();
+  if (pl.nt == 1) return launch_stream<1>(p, pl.nn, pl.waves, st);
+  if (pl.nt == 2) return launch_stream<2>(p, pl.nn, pl.waves, st);
+  if (pl.nt == 4) return launch_stream<4>(p, pl.nn, pl.waves, st);
+  const hipError_t e = pl.split.tile == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
+  if (e != hipSuccess || pl.split.pieces == 1) return e;
+  return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
 }
 
 }  // namespace dmuon
