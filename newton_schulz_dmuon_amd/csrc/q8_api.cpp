@@ -64,6 +64,8 @@ int guarded(F f) {
     return f();
   } catch (const std::exception &e) {
     return fail(DMUON_ERR_INVALID_ARG, "internal error: %s", e.what());
+  } catch (...) {
+    return DMUON_ERR_INVALID_ARG;
   }
 }
 

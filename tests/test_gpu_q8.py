@@ -161,9 +161,11 @@ def test_quantise_every_tie_and_range_end():
 
 # ------------------------------------------------------------- products --
 
+# (the last five: the streaming kernel's block shapes, tiles, tiles split along K)
 PRODUCT_SIZES = [(1, 1, 1), (1, 128, 128), (1, 1001, 513), (2, 16, 4096), (3, 17, 130), (15, 129, 257), (16, 256, 1024),
                  (17, 40, 128), (33, 300, 640), (64, 512, 2048), (65, 130, 1000), (100, 1024, 384), (129, 257, 2100),
-                 (200, 640, 128), (256, 256, 256), (257, 520, 1030), (520, 264, 300), (700, 900, 1)]
+                 (200, 640, 128), (256, 256, 256), (257, 520, 1030), (520, 264, 300), (700, 900, 1), (5, 9000, 130), (40, 8200, 257),
+                 (60, 8200, 260), (1100, 1500, 700), (1100, 300, 6000)]
 
 
 @pytest.mark.parametrize("t,n,k", PRODUCT_SIZES)
@@ -203,7 +205,8 @@ def test_product_of_small_integers(t, n, k, dtype):
 
 WGRAD_SIZES = [(1, 1, 1), (1, 128, 128), (2, 300, 513), (3, 17, 130), (31, 64, 64), (32, 65, 129), (33, 256, 256),
                (64, 257, 200), (65, 40, 1000), (127, 1001, 33), (200, 136, 384), (333, 520, 513), (1000, 129, 257),
-               (1025, 256, 512), (2100, 8, 128)]
+               (1025, 256, 512), (2100, 8, 128),
+               (3000, 700, 300), (450, 8200, 2100)]
 
 
 @pytest.mark.parametrize("t,n,k", WGRAD_SIZES)
@@ -223,6 +226,36 @@ def test_weight_grad(t, n, k, dtype, base):
     check_sum(got, want, mag, t + 1, (t, n, k, base))
     if base == "other":
         assert np.array_equal(host(b), b0)
+
+
+def test_whole_and_split_tiles():
+    """Sizes whose launches hold whole tiles and split ones, against float64
+    products on the GPU of the values that the codes stand for."""
+    print("whole and split tiles", flush=True)
+    t, n, k = 4200, 4301, 8003
+    torch.manual_seed(5)
+    x = torch.randn(t, k, device="cuda").to(BF16)
+    w = (0.02 * torch.randn(n, k, device="cuda")).to(BF16)
+    dy = (0.01 * torch.randn(k, n, device="cuda")).to(BF16)
+    x8, w8 = nsd.q8_quantize(x), nsd.q8_quantize_weights([w])[0]
+
+    def row_vals(q):
+        m = q.codes.shape[0]
+        s = (q.scales[:, :m].t().to(torch.int64) - 127 + 1023 << 52).view(torch.float64)
+        return (q.codes.double() * s.repeat_interleave(128, 1))[:, :q.cols]
+
+    ws = (w8.scales.to(torch.int64) - 127 + 1023 << 52).view(torch.float64)
+    wv = (w8.codes.double() * ws.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1))[:, :k]
+    xv = row_vals(x8)
+    want, mag = (xv @ wv.t()).cpu().numpy(), (xv.abs() @ wv.abs().t()).cpu().numpy()
+    for dtype in (BF16, F32):
+        check_sum(nsd.q8_matmul(x8, w8, dtype=dtype), want, mag, k, dtype, CUT if dtype == BF16 else 0.0)
+    # k rows of n gradients, and of t columns of x^T
+    z8 = nsd.q8_quantize(x.t().contiguous())
+    zv, dv = row_vals(z8), dy.double()
+    want, mag = (dv.t() @ zv).cpu().numpy(), (dv.abs().t() @ zv.abs()).cpu().numpy()
+    for dtype in (BF16, F32):
+        check_sum(nsd.q8_weight_grad(dy, z8, dtype=dtype), want, mag, k, dtype)
 
 
 def test_no_rows():
@@ -250,14 +283,14 @@ def test_non_finite_reach_only_their_outputs(t):
     x = torch.from_numpy(rng.standard_normal((t, k))).to(BF16)
     x[1, 129] = float("nan")
     q = nsd.q8_quantize(x.cuda())
-    y = nsd.q8_matmul(q, w, dtype=F32)
+    y, y16 = nsd.q8_matmul(q, w, dtype=F32), nsd.q8_matmul(q, w)
     dy = torch.from_numpy(rng.standard_normal((t, n)) * 0.01).to(BF16)
     dy[t - 1, 5] = float("inf")
     g = nsd.q8_weight_grad(dy.cuda(), q, dtype=F32)
     torch.cuda.synchronize()
     bad = np.zeros((t, n), bool)
     bad[1] = True
-    assert np.array_equal(np.isnan(host(y)), bad)
+    assert np.array_equal(np.isnan(host(y)), bad) and np.array_equal(np.isnan(host(y16)), bad)
     gh = host(g)
     assert np.isnan(gh[:, 129]).all()
     others = np.delete(np.delete(gh, 129, axis=1), 5, axis=0)
@@ -267,6 +300,61 @@ def test_non_finite_reach_only_their_outputs(t):
     row = np.delete(gh[5], 129)
     assert np.isnan(row[last == 0]).all()
     assert np.array_equal(row[last != 0], np.sign(last[last != 0]) * np.inf)
+
+
+@pytest.mark.parametrize("t", [3, 70, 300])
+def test_non_finite_last_row(t):
+    """NaN in the last row (whose copies stand in for the rows behind it) and
+    an infinity in the gradient's: each reaches its column, and no other."""
+    print(f"non-finite last row {t}", flush=True)
+    rng = np.random.default_rng(t)
+    n, k = 130, 300
+    x = torch.from_numpy(rng.standard_normal((t, k))).to(BF16)
+    x[t - 1, 7] = float("inf")
+    dy = torch.from_numpy(rng.standard_normal((t, n)) * 0.01).to(BF16)
+    dy[t - 1, 129] = float("nan")
+    q = nsd.q8_quantize(x.cuda())
+    w, _ = weight_of(rng, n, k)
+    for dtype in (BF16, F32):
+        g = host(nsd.q8_weight_grad(dy.cuda(), q, dtype=dtype))
+        bad = np.zeros((n, k), bool)
+        bad[129], bad[:, 7] = True, True
+        assert np.array_equal(np.isnan(g), bad)
+        y = host(nsd.q8_matmul(q, w, dtype=dtype))
+        assert np.isnan(y[t - 1]).all() and np.isfinite(y[:t - 1]).all()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 codes: the rows at the far end, alone and in the
+    gradient, where all other rows are zero."""
+    print("offsets beyond 32 bits", flush=True)
+    t, k, n, far = (1 << 20) + 5, 4224, 40, 70
+    rng = np.random.default_rng(77)
+    x = torch.zeros(t, k, dtype=BF16, device="cuda")
+    xf = values(rng, far, k, BF16)
+    x[t - far:] = xf.cuda()
+    q = nsd.q8_quantize(x)
+    del x
+    codes, scales = ref.quantize_rows(host(xf))
+    check_codes(q.codes[t - far:], codes, "codes")
+    check_bytes(q.scales[:, t - far:t], scales[:, :far], "scales")
+    assert not q.codes[:1000].view(torch.uint8).any() and (q.scales[:, :1000] == 10).all()
+    w, wv = weight_of(rng, n, k)
+    xv = ref.row_values(codes, scales)[:, :k]
+    y = nsd.q8_matmul(q, w, dtype=F32)
+    check_sum(y[t - far:], *ref.matmul(xv, wv), k, "product")
+    assert not y[:t - far].any()
+    # as rows of the result: more than 2^32 outputs
+    w2, _ = weight_of(rng, k, 8)
+    one = nsd.q8_quantize(torch.ones(t, 8, dtype=BF16, device="cuda"))
+    y2 = nsd.q8_matmul(one, w2)
+    assert torch.equal(y2[t - 1], y2[0]) and torch.equal(y2[t // 2], y2[0]) and y2[0].any()
+    del y2
+    dy = torch.zeros(t, n, dtype=BF16, device="cuda")
+    dyf = values(rng, far, n, BF16)
+    dy[t - far:] = dyf.cuda()
+    g = nsd.q8_weight_grad(dy, q, dtype=F32)
+    check_sum(g, *ref.weight_grad(host(dyf), xv), far, "gradient")
 
 
 def test_extreme_scales():
