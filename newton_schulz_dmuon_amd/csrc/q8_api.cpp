@@ -12,12 +12,15 @@
 namespace dmuon {
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+// A launch takes fewer than 2^32 threads along its grid.  With these limits the
+// products' grids stay below that: at most 2^22 tiles of 128, or with 2^37
+// outputs 2^21 whole and as many ragged tiles of 256, of 512 threads each.
+constexpr int64_t kMaxRows = int64_t(1) << 29;
 constexpr int64_t kMaxSide = int64_t(1) << 22;
-constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxElems = int64_t(1) << 37;
 
-// Rows x cols whose product stays within kMaxElems (both factors are at most
-// 2^31, so the product cannot overflow).
+// Whether a buffer has more than kMaxElems elements (the factors are within the
+// limits above, so the product cannot overflow).
 bool too_large(int64_t rows, int64_t cols) { return rows * cols > kMaxElems; }
 
 int check_sizes(int64_t rows, int64_t outs, int64_t cols) {
@@ -26,7 +29,7 @@ int check_sizes(int64_t rows, int64_t outs, int64_t cols) {
   if (cols < 1 || cols > kMaxSide) return fail(DMUON_ERR_INVALID_ARG, "columns %lld", (long long)cols);
   const int64_t kp = round_up(cols, kQ8Block), np = round_up(outs, kQ8Block);
   if (too_large(rows, kp) || too_large(rows, outs) || too_large(np, kp))
-    return fail(DMUON_ERR_INVALID_ARG, "%lld rows, %lld outputs, %lld columns: a buffer exceeds 2^40 elements",
+    return fail(DMUON_ERR_INVALID_ARG, "%lld rows, %lld outputs, %lld columns: a buffer exceeds 2^37 elements",
                 (long long)rows, (long long)outs, (long long)cols);
   return DMUON_OK;
 }
@@ -104,7 +107,8 @@ int dmuon_q8_quantize_weights(const dmuon_q8_weight *w, int32_t n, void *stream)
     int rc;
     for (int32_t i = 0; i < n; ++i) {
       const dmuon_q8_weight &d = w[i];
-      if (d.rows < 1 || d.rows > kMaxSide || d.cols < 1 || d.cols > kMaxSide || too_large(d.rows, d.cols))
+      if (d.rows < 1 || d.rows > kMaxSide || d.cols < 1 || d.cols > kMaxSide || 
+          too_large(round_up(d.rows, kQ8Block), round_up(d.cols, kQ8Block)))
         return fail(DMUON_ERR_INVALID_ARG, "matrix %d: bad shape %lld x %lld", i, (long long)d.rows,
                     (long long)d.cols);
       if (!dtype_ok(d.param_dtype))
@@ -136,12 +140,12 @@ int dmuon_q8_quantize_weights(const dmuon_q8_weight *w, int32_t n, void *stream)
       batch.rows[k] = d.rows;
       batch.cols[k] = d.cols;
       batch.param_dt[k] = d.param_dtype;
-      // a matrix has at most 2^40 / 2^14 blocks plus its ragged edge's, so a
-      // batch's count fits a grid's 32 bits
+      // a matrix has at most 2^37 / 2^14 blocks, so a batch's threads stay
+      // below 2^32
       batch.first_block[k + 1] = batch.first_block[k] + (round_up(d.rows, kQ8Block) / kQ8Block) *
                                                             (round_up(d.cols, kQ8Block) / kQ8Block);
       batch.n = k + 1;
-      if (batch.n == kQ8Batch || i + 1 == n || batch.first_block[batch.n] > 0x3fffffff) {
+      if (batch.n == kQ8Batch || i + 1 == n || batch.first_block[batch.n] > (1 << 22)) {
         rc = check_launch(launch_q8_weights(batch, static_cast<hipStream_t>(stream)), "q8 weights launch");
         if (rc) return rc;
         std::memset(&batch, 0, sizeof batch);

@@ -75,7 +75,7 @@ __device__ __forceinline__ TileWork tile_work(const TileSplit &sp, uint32_t w, u
     const uint32_t r = w - sp.whole, piece = uniform(r / sp.tail), place = uniform(r - piece * sp.tail);
     idx = sp.whole + xcd_order(place, sp.tail);
     if (sp.pieces > 1) {
-      // steps * pieces fits 32 bits: 2^25 steps, 2^4 pieces
+      // steps * pieces fits 32 bits: 2^23 steps, 2^4 pieces
       t.begin = static_cast<int>(uniform(steps * piece / sp.pieces));
       t.end = static_cast<int>(uniform(steps * (piece + 1) / sp.pieces));
       t.slot = static_cast<int64_t>(idx - sp.whole) * sp.pieces + piece;

@@ -466,10 +466,9 @@ hipError_t launch_stream(const Q8Product &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int NT>
-hipError_t launch_stream(const Q8Product &p, int nn, int waves, hipStream_t st) {
-  if (nn == 2) return waves == 4 ? launch_stream<NT, 2, 4>(p, st) : launch_stream<NT, 2, 8>(p, st);
-  return waves == 4 ? launch_stream<NT, 1, 4>(p, st) : launch_stream<NT, 1, 8>(p, st);
+template <int NT, int WAVES>
+hipError_t launch_stream(const Q8Product &p, int nn, hipStream_t st) {
+  return nn == 2 ? launch_stream<NT, 2, WAVES>(p, st) : launch_stream<NT, 1, WAVES>(p, st);
 }
 
 }  // namespace
@@ -480,9 +479,9 @@ size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_d
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
   const Plan pl = plan_of(p.rows, p.outs, p.kp, p.out_dt);
-  if (pl.nt == 1) return launch_stream<1>(p, pl.nn, pl.waves, st);
-  if (pl.nt == 2) return launch_stream<2>(p, pl.nn, pl.waves, st);
-  if (pl.nt == 4) return launch_stream<4>(p, pl.nn, pl.waves, st);
+  if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, pl.nn, st) : launch_stream<1, 4>(p, pl.nn, st);
+  if (pl.nt == 2) return launch_stream<2, 4>(p, pl.nn, st);
+  if (pl.nt == 4) return launch_stream<4, 4>(p, pl.nn, st);
   const hipError_t e = pl.split.tile == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
   if (e != hipSuccess || pl.split.pieces == 1) return e;
   return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);

@@ -13,6 +13,8 @@
 // Both kernels are one pass over the data and bound by HBM: every element is
 // read once and every code written once.
 
+#include <algorithm>
+
 #include "q8_device.h"
 
 namespace dmuon {
@@ -20,6 +22,8 @@ namespace dmuon {
 namespace {
 
 constexpr int kThreads = 256;
+// Rows per launch: its threads along the grid stay below 2^32.
+constexpr int64_t kLaunchRows = int64_t(1) << 24;
 
 // |v| as ordered bits, 0 for NaN and infinities.
 __device__ __forceinline__ uint32_t finite_magnitude(float v) {
@@ -117,11 +121,11 @@ __device__ __forceinline__ void load_patch(const void *x, int64_t t, int64_t c, 
 // [block][row] table.  Rows behind the last are zero rows (scale byte of a zero
 // block).
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void q8_rows_kernel(const void *__restrict__ x, int64_t rows, int64_t cols,
-                                                           int64_t kp, uint8_t *__restrict__ codes,
+__global__ __launch_bounds__(kThreads) void q8_rows_kernel(const void *__restrict__ x, int64_t first, int64_t rows,
+                                                           int64_t cols, int64_t kp, uint8_t *__restrict__ codes,
                                                            uint8_t *__restrict__ scales, int64_t t4) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4;
+  const int64_t t = first + static_cast<int64_t>(blockIdx.x) * 4;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * 512 + lane * 8;
   if (c >= kp) return;
   float v[4][8];
@@ -237,12 +241,16 @@ hipError_t launch_q8_rows(const void *x, int32_t dt, int64_t rows, int64_t cols,
                           hipStream_t st) {
   const int64_t kp = (cols + kQ8Block - 1) / kQ8Block * kQ8Block;
   const int64_t t4 = (rows + kQ8ScaleRow - 1) / kQ8ScaleRow * kQ8ScaleRow;
-  const dim3 grid(static_cast<uint32_t>(t4 / 4), static_cast<uint32_t>((kp + 2047) / 2048));
-  if (dt == kF32)
-    hipLaunchKernelGGL(q8_rows_kernel<true>, grid, dim3(kThreads), 0, st, x, rows, cols, kp, codes, scales, t4);
-  else
-    hipLaunchKernelGGL(q8_rows_kernel<false>, grid, dim3(kThreads), 0, st, x, rows, cols, kp, codes, scales, t4);
-  return hipGetLastError();
+  for (int64_t first = 0; first < t4; first += kLaunchRows) {
+    const dim3 grid(static_cast<uint32_t>(std::min(t4 - first, kLaunchRows) / 4), static_cast<uint32_t>((kp + 2047) / 2048));
+    if (dt == kF32)
+      hipLaunchKernelGGL(q8_rows_kernel<true>, grid, dim3(kThreads), 0, st, x, first, rows, cols, kp, codes, scales, t4);
+    else
+      hipLaunchKernelGGL(q8_rows_kernel<false>, grid, dim3(kThreads), 0, st, x, first, rows, cols, kp, codes, scales, t4);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_q8_weights(const Q8WeightBatch &b, hipStream_t st) {

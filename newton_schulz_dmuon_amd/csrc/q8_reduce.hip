@@ -51,6 +51,8 @@ TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCost
       if (tile == 256) return c.low256 + (c.full256 - c.low256) * static_cast<float>(std::min(n, kCus)) / kCus;
       return n <= kCus ? c.one128 : c.two128;
     };
+    // a launch's threads stay below 2^32
+    if (tile == 128 && best.tile && tiles > (1 << 22)) continue;
     const int64_t rounds = tiles / slots, left = tiles - rounds * slots;
     const float whole_us = static_cast<float>(rounds * steps) * step_us(slots);
     for (const int64_t pieces : {1, 2, 3, 4, 6, 8, 12, 16}) {

@@ -8,6 +8,8 @@
 // is expanded to bf16 on its way into LDS and multiplied with the bf16
 // gradient; sums are fp32.
 
+#include <algorithm>
+
 #include "q8_device.h"
 
 namespace dmuon {
@@ -150,7 +152,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   // x: a thread of half 0 takes FM columns (a run) by eight rows of t (a group:
   // one chunk of LDS); columns behind the last block are clamped to it.
   // Offsets from a step's uniform base fit 32 bits: 64 rows of at most 2^22
-  // codes, and two scale rows of at most 2^31 bytes.
+  // codes, and two scale rows of at most 2^29 bytes.
   constexpr int kWords = FM / 4;
   typedef uint32_t Run __attribute__((ext_vector_type(kWords)));
   typedef __attribute__((address_space(1))) Run g_Run;
@@ -369,25 +371,31 @@ void q8_wgrad_kernel(Q8WeightGrad p, TileSplit sp) {
   }
 }
 
+// Work-groups of the two kernels below, 2048 elements each at a time: their
+// threads stay below 2^32 whatever the size.
+uint32_t element_groups(int64_t n) { return static_cast<uint32_t>(std::min<int64_t>((n + 2047) / 2048, 1 << 20)); }
+
 // No rows: out = base, or zero.
 __global__ __launch_bounds__(256) void q8_wgrad_empty_kernel(Q8WeightGrad p) {
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int64_t left = p.outs * p.cols - at;
-  if (left > 0) finish_run<8>(p.base, p.out, p.out_dt, at, left, true, v);
+  const int64_t n = p.outs * p.cols;
+  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; at < n; at += gridDim.x * int64_t(2048)) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    finish_run<8>(p.base, p.out, p.out_dt, at, n - at, true, v);
+  }
 }
 
 // A copy of dy with rows of a multiple of 8 elements (zeros behind the last
 // column), for a dy whose rows are not: the LDS-bound loads take 16 bytes.
 __global__ __launch_bounds__(256) void q8_pad_rows_kernel(const uint16_t *__restrict__ dy, int64_t rows, int64_t cols,
                                                           int64_t ld, uint16_t *__restrict__ out) {
-  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (at >= rows * ld) return;
-  const int64_t t = at / ld, c = at - t * ld;
-  uint32_t e[8];
+  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; at < rows * ld;
+       at += gridDim.x * int64_t(2048)) {
+    const int64_t t = at / ld, c = at - t * ld;
+    uint32_t e[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) e[k] = c + k < cols ? ((const g_u16 *)dy)[t * cols + c + k] : 0;
-  *(g_u32x4 *)(out + at) = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    for (int k = 0; k < 8; ++k) e[k] = c + k < cols ? ((const g_u16 *)dy)[t * cols + c + k] : 0;
+    *(g_u32x4 *)(out + at) = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+  }
 }
 
 // Microseconds a step of 64 rows, measured on 8192 rows: 1.5 with one
@@ -423,15 +431,13 @@ size_t q8_wgrad_workspace(int64_t rows, int64_t outs, int64_t cols) {
 hipError_t launch_q8_wgrad(const Q8WeightGrad &args, hipStream_t st) {
   Q8WeightGrad p = args;
   if (p.rows == 0) {
-    hipLaunchKernelGGL(q8_wgrad_empty_kernel, dim3(static_cast<uint32_t>((p.outs * p.cols + 2047) / 2048)), dim3(256), 0,
-                       st, p);
+    hipLaunchKernelGGL(q8_wgrad_empty_kernel, dim3(element_groups(p.outs * p.cols)), dim3(256), 0, st, p);
     return hipGetLastError();
   }
   const Plan pl = plan_of(p.rows, p.outs, p.cols);
   p.dy_ld = pl.dy_ld;
   if (pl.pad_bytes) {
-    const int64_t groups = (p.rows * pl.dy_ld / 8 + 255) / 256;
-    hipLaunchKernelGGL(q8_pad_rows_kernel, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, st,
+    hipLaunchKernelGGL(q8_pad_rows_kernel, dim3(element_groups(p.rows * pl.dy_ld)), dim3(256), 0, st,
                        static_cast<const uint16_t *>(p.dy), p.rows, p.outs, pl.dy_ld, static_cast<uint16_t *>(p.ws));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

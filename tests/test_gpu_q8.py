@@ -324,6 +324,40 @@ def test_non_finite_last_row(t):
         assert np.isnan(y[t - 1]).all() and np.isfinite(y[:t - 1]).all()
 
 
+def test_more_rows_than_one_launch():
+    """More than 2^24 rows are quantised by several launches; a gradient of
+    more than 2^31 elements is padded and cleared by a capped grid."""
+    print("more rows than one launch", flush=True)
+    t, k, n, far = (1 << 26) + 5, 3, 33, 70
+    rng = np.random.default_rng(78)
+    x = torch.zeros(t, k, dtype=BF16, device="cuda")
+    edges = [values(rng, far, k, BF16) for _ in range(2)]
+    starts = (1 << 24) - 30, t - far
+    for at, e in zip(starts, edges):
+        x[at:at + far] = e.cuda()
+    q = nsd.q8_quantize(x)
+    del x
+    xv = []
+    for at, e in zip(starts, edges):
+        codes, scales = ref.quantize_rows(host(e))
+        check_codes(q.codes[at:at + far], codes, "codes")
+        check_bytes(q.scales[:, at:at + far], scales[:, :far], "scales")
+        xv.append(ref.row_values(codes, scales)[:, :k])
+    dy = torch.zeros(t, n, dtype=BF16, device="cuda")
+    dyv = []
+    for at in starts:
+        d = values(rng, far, n, BF16)
+        dy[at:at + far] = d.cuda()
+        dyv.append(host(d))
+    g = nsd.q8_weight_grad(dy, q, dtype=F32)
+    check_sum(g, *ref.weight_grad(np.concatenate(dyv), np.concatenate(xv)), 2 * far, "gradient")
+    del dy, q
+    out = torch.full(((1 << 16) + 8, (1 << 15) + 3), 3.0, dtype=BF16, device="cuda")
+    empty = nsd.q8_quantize(torch.empty(0, out.shape[1], dtype=BF16, device="cuda"))
+    nsd.q8_weight_grad(torch.empty(0, out.shape[0], dtype=BF16, device="cuda"), empty, out=out)
+    assert not out.any()
+
+
 def test_offsets_beyond_32_bits():
     """More than 2^32 codes: the rows at the far end, alone and in the
     gradient, where all other rows are zero."""

@@ -144,3 +144,19 @@ def test_binding_shapes():
     assert w.codes_t.shape == (300, 256) and w.scales_t.shape == (3, 2)
     assert nsd.Q8Weight.empty(130, 300, "cpu", transposed=False).codes_t is None
     assert nsd.q8_quantize_weights([]) == []
+
+
+def test_size_limits(lib):
+    """Sizes that a launch could not count are refused: rows beyond 2^29, and
+    buffers of more than 2^37 elements."""
+    ref = ctypes.byref(ctypes.c_size_t(0))
+    assert quantize(lib, rows=(1 << 29) + 1, cols=1) == _lib.ERR_INVALID_ARG
+    assert quantize(lib, rows=(1 << 27) + 1, cols=1000) == _lib.ERR_INVALID_ARG
+    big = (_lib.Q8WeightDesc * 1)(weight(rows=1 << 22, cols=(1 << 15) + 1))
+    assert lib.dmuon_q8_quantize_weights(big, 1, None) == _lib.ERR_INVALID_ARG
+    for fn, extra in ((lib.dmuon_q8_matmul_workspace_bytes, (_lib.BF16,)),
+                      (lib.dmuon_q8_weight_grad_workspace_bytes, ())):
+        assert fn(1 << 29, 256, 256, *extra, ref) == _lib.OK
+        assert fn((1 << 29) + 1, 1, 1, *extra, ref) == _lib.ERR_INVALID_ARG
+        assert fn(1 << 29, 257, 1, *extra, ref) == _lib.ERR_INVALID_ARG
+        assert fn(1, 1 << 22, (1 << 15) + 1, *extra, ref) == _lib.ERR_INVALID_ARG
