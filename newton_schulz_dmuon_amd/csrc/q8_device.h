@@ -94,10 +94,10 @@ struct TileOut {
   int64_t at, ld;   // the tile's first element, and a row's length
   int64_t rows, cols;  // of the tile that exist
 };
-__device__ __forceinline__ TileOut tile_out(const TileWork &w, int tile, const void *base, void *out, int32_t dt,
+__device__ __forceinline__ TileOut tile_out(const TileWork &w, int ta, int tb, const void *base, void *out, int32_t dt,
                                             int64_t rows, int64_t cols, void *ws) {
-  if (w.slot >= 0) return TileOut{nullptr, ws, kF32, w.slot * tile * tile, tile, tile, tile};
-  const int64_t r = static_cast<int64_t>(w.b) * tile, c = static_cast<int64_t>(w.a) * tile;
+  if (w.slot >= 0) return TileOut{nullptr, ws, kF32, w.slot * ta * tb, ta, tb, ta};
+  const int64_t r = static_cast<int64_t>(w.b) * tb, c = static_cast<int64_t>(w.a) * ta;
   return TileOut{base, out, dt, r * cols + c, cols, rows - r, cols - c};
 }
 

@@ -4,6 +4,8 @@
 // C ABI.
 #pragma once
 
+#include <initializer_list>
+
 #include "internal.h"
 
 namespace dmuon {
@@ -34,26 +36,29 @@ hipError_t launch_q8_rows(const void *x, int32_t dt, int64_t rows, int64_t cols,
                           uint8_t *scales, hipStream_t st);
 hipError_t launch_q8_weights(const Q8WeightBatch &b, hipStream_t st);
 
-// How a product's tile x tile output tiles (na across, nb down) are shared out:
-// the first `whole` of them one work-group each, the last `tail` split into
-// `pieces` along the sum, whose fp32 results go to tile x tile slots of the
+// How a product's output tiles (ta columns by tb rows; na across, nb down) are
+// shared out: the first `whole` of them one work-group each, the last `tail`
+// split into `pieces` along the sum, whose fp32 results go to slots of the
 // workspace, [tail tile][piece], and are added by a reduce launch.
 struct TileSplit {
-  uint32_t tile, na, nb;
+  uint32_t ta, tb, na, nb;
   uint32_t whole, tail, pieces;
   size_t ws_bytes() const {
-    return pieces > 1 ? size_t(tail) * pieces * tile * tile * sizeof(float) : 0;
+    return pieces > 1 ? size_t(tail) * pieces * ta * tb * sizeof(float) : 0;
   }
 };
 
-// What a launch of tiles costs, in microseconds, as measured (the kernels say
-// where): a step of a work-group with the chip nearly empty and full, for the
-// 256-tile (one work-group a CU) and the 128-tile (one, and two a CU).
-struct TileCosts {
-  float low256, full256, one128, two128;
+// A tile that a kernel can take, and what a step of its work-group costs in
+// microseconds, as measured (the kernels say where): for one work-group a CU,
+// with the chip nearly empty and full; for two, with one and two on each CU.
+struct TileCost {
+  int64_t ta, tb, per_cu;
+  float low, full;
 };
-// The cheapest of the splits by that measure; steps of the sum.
-TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCosts &c, float *cost = nullptr);
+// The cheapest tile and split by that measure; steps of the sum.  Tiles are
+// listed from the largest down.
+TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, std::initializer_list<TileCost> tiles,
+                       float *cost = nullptr);
 
 // out[r][c] = base[r][c] (0 if null) + the sum of the pieces' results, in order,
 // rounded once to dt, over the tail tiles of a split.  base may be out.

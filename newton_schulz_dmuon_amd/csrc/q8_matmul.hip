@@ -372,7 +372,7 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
-  const TileOut o = tile_out(w, TS, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
+  const TileOut o = tile_out(w, TS, TS, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
   const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
@@ -397,7 +397,8 @@ namespace {
 // with one work-group on the chip and 1.5 with 256 (the clock gives way), a
 // 128-tile 0.6 alone on its CU and 1.06 for two; fp32 results 2.23 and 2.9,
 // 0.94 and 1.88.
-constexpr TileCosts kBf16Costs = {1.03f, 1.5f, 0.6f, 1.06f}, kExactCosts = {2.23f, 2.9f, 0.95f, 1.88f};
+constexpr std::initializer_list<TileCost> kBf16Costs = {{256, 256, 1, 1.03f, 1.5f}, {128, 128, 2, 0.6f, 1.06f}},
+                                          kExactCosts = {{256, 256, 1, 2.23f, 2.9f}, {128, 128, 2, 0.95f, 1.88f}};
 
 // How a product runs: streamed (row blocks and waves of a work-group) or in
 // tiles.
@@ -482,7 +483,7 @@ hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
   if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, pl.nn, st) : launch_stream<1, 4>(p, pl.nn, st);
   if (pl.nt == 2) return launch_stream<2, 4>(p, pl.nn, st);
   if (pl.nt == 4) return launch_stream<4, 4>(p, pl.nn, st);
-  const hipError_t e = pl.split.tile == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
+  const hipError_t e = pl.split.ta == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
   if (e != hipSuccess || pl.split.pieces == 1) return e;
   return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
 }

@@ -16,22 +16,22 @@ constexpr int64_t kCus = 256;
 // holds the pieces' results, each read once: with their writing 6 TB/s.
 __global__ __launch_bounds__(256) void q8_reduce_kernel(const float *__restrict__ ws, TileSplit sp, int64_t rows,
                                                         int64_t cols, const void *base, void *out, int32_t dt) {
-  const uint32_t per = sp.tile * sp.tile / 2048;
+  const uint32_t size = sp.ta * sp.tb, per = size / 2048;
   const uint32_t place = uniform(blockIdx.x / per), part = blockIdx.x - place * per;
   uint32_t a, b;
   tile_at(sp.whole + place, sp.na, sp.nb, a, b);
   const uint32_t at = (part * 256 + threadIdx.x) * 8;
-  const uint32_t shift = sp.tile == 256 ? 8 : 7;
-  const int64_t r = static_cast<int64_t>(b) * sp.tile + (at >> shift);
-  const int64_t c = static_cast<int64_t>(a) * sp.tile + (at & (sp.tile - 1));
+  const uint32_t shift = sp.ta == 256 ? 8 : 7;
+  const int64_t r = static_cast<int64_t>(b) * sp.tb + (at >> shift);
+  const int64_t c = static_cast<int64_t>(a) * sp.ta + (at & (sp.ta - 1));
   if (r >= rows || c >= cols) return;
-  const float *const src = ws + static_cast<int64_t>(place) * sp.pieces * sp.tile * sp.tile + at;
+  const float *const src = ws + static_cast<int64_t>(place) * sp.pieces * size + at;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (uint32_t i = 0; i < sp.pieces; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const f32x4 w = *(const g_f32x4 *)(src + static_cast<int64_t>(i) * sp.tile * sp.tile + 4 * h);
+      const f32x4 w = *(const g_f32x4 *)(src + static_cast<int64_t>(i) * size + 4 * h);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[4 * h + k] += w[k];
     }
@@ -40,20 +40,21 @@ __global__ __launch_bounds__(256) void q8_reduce_kernel(const float *__restrict_
 
 }  // namespace
 
-TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCosts &c, float *cost) {
+TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, std::initializer_list<TileCost> tiles,
+                       float *cost) {
   TileSplit best{};
   float best_us = 0.f;
-  for (const int64_t tile : {int64_t(256), int64_t(128)}) {
-    const int64_t na = (cols + tile - 1) / tile, nb = (rows + tile - 1) / tile, tiles = na * nb;
-    const int64_t slots = tile == 256 ? kCus : 2 * kCus;  // work-groups on the chip at once
+  for (const TileCost &c : tiles) {
+    const int64_t na = (cols + c.ta - 1) / c.ta, nb = (rows + c.tb - 1) / c.tb, count = na * nb;
+    const int64_t slots = c.per_cu * kCus;  // work-groups on the chip at once
     // a step's time with this many work-groups on the chip
     auto step_us = [&](int64_t n) {
-      if (tile == 256) return c.low256 + (c.full256 - c.low256) * static_cast<float>(std::min(n, kCus)) / kCus;
-      return n <= kCus ? c.one128 : c.two128;
+      if (c.per_cu == 1) return c.low + (c.full - c.low) * static_cast<float>(std::min(n, kCus)) / kCus;
+      return n <= kCus ? c.low : c.full;
     };
     // a launch's threads stay below 2^32
-    if (tile == 128 && best.tile && tiles > (1 << 22)) continue;
-    const int64_t rounds = tiles / slots, left = tiles - rounds * slots;
+    if (best.ta && count > (1 << 22)) continue;
+    const int64_t rounds = count / slots, left = count - rounds * slots;
     const float whole_us = static_cast<float>(rounds * steps) * step_us(slots);
     for (const int64_t pieces : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (pieces > steps || (pieces > 1 && left == 0)) break;
@@ -63,13 +64,14 @@ TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCost
       us += static_cast<float>(full * piece_steps) * step_us(slots);
       if (rest) us += static_cast<float>(piece_steps) * step_us(rest);
       // the reduce launch: every piece's result written and read at 6 TB/s
-      if (pieces > 1) us += 3.5f + static_cast<float>(groups * tile * tile * 8) / 6e6f;
-      if (best.tile == 0 || us < best_us) {
+      if (pieces > 1) us += 3.5f + static_cast<float>(groups * c.ta * c.tb * 8) / 6e6f;
+      if (best.ta == 0 || us < best_us) {
         best_us = us;
-        best.tile = static_cast<uint32_t>(tile);
+        best.ta = static_cast<uint32_t>(c.ta);
+        best.tb = static_cast<uint32_t>(c.tb);
         best.na = static_cast<uint32_t>(na);
         best.nb = static_cast<uint32_t>(nb);
-        best.whole = static_cast<uint32_t>(pieces > 1 ? rounds * slots : tiles);
+        best.whole = static_cast<uint32_t>(pieces > 1 ? rounds * slots : count);
         best.tail = static_cast<uint32_t>(pieces > 1 ? left : 0);
         best.pieces = static_cast<uint32_t>(pieces);
       }
@@ -81,7 +83,7 @@ TileSplit choose_split(int64_t cols, int64_t rows, int64_t steps, const TileCost
 
 hipError_t launch_q8_reduce(const float *ws, const TileSplit &sp, int64_t rows, int64_t cols, const void *base,
                             void *out, int32_t dt, hipStream_t st) {
-  const uint32_t grid = sp.tail * (sp.tile * sp.tile / 2048);
+  const uint32_t grid = sp.tail * (sp.ta * sp.tb / 2048);
   hipLaunchKernelGGL(q8_reduce_kernel, dim3(grid), dim3(256), 0, st, ws, sp, rows, cols, base, out, dt);
   return hipGetLastError();
 }

@@ -64,8 +64,8 @@ __device__ __forceinline__ void write_lds(uint32_t lds_addr, const u32x4 &v) {
   asm volatile("ds_write_b128 %0, %1 offset:%2" : : "v"(lds_addr), "v"(v), "n"(OFFSET) : "memory");
 }
 
-// TS x TS outputs (TS columns k of x by TS columns n of dy) per work-group of
-// 8 waves (2 x 4), each wave TS/2 k by TS/4 n, in steps of 64 t.  The two
+// TK x TN outputs (columns k of x by columns n of dy) per work-group of
+// 8 waves (2 x 4), each wave TK/2 k by TN/4 n, in steps of 64 t.  The two
 // halves of the work-group (H = 0, 1) run in ping-pong, one reading fragments
 // while the other multiplies, switching at every barrier; H = 1 runs one phase
 // late.  The halves are separate code, so that the compiler can count each
@@ -87,19 +87,19 @@ __device__ __forceinline__ void write_lds(uint32_t lds_addr, const u32x4 &v) {
 // dy, a ring of three stages: half 1 issues the loads of step t + 2 in its read
 // phase of t and waits for them at the end of its read phase of t + 1, before
 // either half reads them.  A stage is only written once both halves have read
-// it.  Together the rings are all of a CU's 160 KB for TS = 256.
+// it.  Together the rings are all of a CU's 160 KB for 256 x 256.
 //
 // Row q of x's 16-row block i of a wave's half holds column ((q % 4) * 4 +
 // q / 4) * FM + i, so that a lane's results (row 4 g + v of its blocks) are
 // FM consecutive columns.  A row's 16-byte chunk (8 t) is XORed with
 // (q / 2) ^ (q % 2), which spreads over the banks the 16 rows of a fragment
 // read as well as eight neighbouring lanes of a write, FM columns apart.
-template <int TS, int H>
+template <int TK, int TN, int H>
 __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8WeightGrad &p, int64_t k0, int64_t n0,
-                                              int tbeg, int tend, f32x4 (&acc)[TS / 32][TS / 64]) {
-  constexpr int FM = TS / 32, FN = TS / 64, kHalves = TS / 128;
-  constexpr int kOperand = kHalves * kHalfBytes;
-  constexpr int kDyLoads = kOperand / 1024 / 4;                // LDS-bound loads of dy per wave of half 1 and step
+                                              int tbeg, int tend, f32x4 (&acc)[TK / 32][TN / 64]) {
+  constexpr int FM = TK / 32, FN = TN / 64, kHalves = TN / 128;
+  constexpr int kXBytes = TK / 128 * kHalfBytes, kDyBytes = kHalves * kHalfBytes;  // of a stage
+  constexpr int kDyLoads = kDyBytes / 1024 / 4;                // LDS-bound loads of dy per wave of half 1 and step
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 3;
@@ -116,9 +116,9 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   auto rows_left = [&](int step) {
     return static_cast<int>(min(p.rows - static_cast<int64_t>(step) * kStep, static_cast<int64_t>(kStep)));
   };
-  lds_char *const dy_lds = lds + 2 * kOperand;
+  lds_char *const dy_lds = lds + 2 * kXBytes;
   auto issue_dy = [&](int slot, int step) {
-    lds_char *const st = dy_lds + slot * kOperand + wn * 1024;
+    lds_char *const st = dy_lds + slot * kDyBytes + wn * 1024;
     const char *const src = static_cast<const char *>(p.dy) + static_cast<int64_t>(step) * kStep * ld;
     const int left = rows_left(step);
     auto load = [&](const char *from, int j) {
@@ -143,7 +143,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   auto zero_tail = [&](int slot, int step) {
     const int left = rows_left(step);
     if (left == kStep) return;
-    lds_char *const st = dy_lds + slot * kOperand + wn * 1024 + lane * 16;
+    lds_char *const st = dy_lds + slot * kDyBytes + wn * 1024 + lane * 16;
 #pragma unroll
     for (int j = 0; j < kDyLoads; ++j)
       if (drow + 16 * (j & 3) >= left) *(lds_u32x4 *)(st + j * 4096) = u32x4{0, 0, 0, 0};
@@ -159,7 +159,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   const int run = tid & 31, group = (tid & 255) >> 5;
   const int64_t t4 = (p.rows + 3) & ~static_cast<int64_t>(3);
   const uint32_t xcol =
-      min(static_cast<uint32_t>(FM * run), static_cast<uint32_t>(min(p.kp - FM - k0, static_cast<int64_t>(TS))));
+      min(static_cast<uint32_t>(FM * run), static_cast<uint32_t>(min(p.kp - FM - k0, static_cast<int64_t>(TK))));
   const uint32_t scol = xcol / kQ8Block * static_cast<uint32_t>(t4);
   Run codes[8];
   uint32_t sword[2];
@@ -182,11 +182,11 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   {
     const int r = run & 15, row = (r & 3) * 4 + (r >> 2);
     x_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) +
-           static_cast<uint32_t>(((run >> 4) * (TS / 2) + row) * 128 + ((group ^ (row >> 1) ^ (row & 1)) & 7) * 16);
+           static_cast<uint32_t>(((run >> 4) * (TK / 2) + row) * 128 + ((group ^ (row >> 1) ^ (row & 1)) & 7) * 16);
   }
   // expands and transposes the loaded codes into stage `slot`
   auto write_x = [&](int slot) {
-    const uint32_t at = x_at + static_cast<uint32_t>(slot * kOperand);
+    const uint32_t at = x_at + static_cast<uint32_t>(slot * kXBytes);
 #pragma unroll
     for (int c = 0; c < kWords; ++c) {
       uint32_t lo[8], hi[8];  // columns 4 c, 4 c + 1 and 4 c + 2, 4 c + 3 of row j
@@ -243,7 +243,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
     return static_cast<uint32_t>(r * 128 + (((l >> 4) ^ (r >> 1) ^ (r & 1)) & 7) * 16);
   };
   auto read_x = [&](const lds_char *op, uint32_t xb, int i, int s) {
-    return *(const lds_u32x4 *)(op + (H * (TS / 2) + i * 16) * 128 + (xb ^ (s * 64)));
+    return *(const lds_u32x4 *)(op + (H * (TK / 2) + i * 16) * 128 + (xb ^ (s * 64)));
   };
 
   const int last = tend - 1;
@@ -262,7 +262,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   lds_barrier();
   if (H == 1) barrier();
   for (int t = tbeg; t < tend; ++t) {
-    const lds_char *const xs = lds + (t & 1) * kOperand, *const ds = dy_lds + s0 * kOperand;
+    const lds_char *const xs = lds + (t & 1) * kXBytes, *const ds = dy_lds + s0 * kDyBytes;
     // the last steps load and write the last rows again, into free stages,
     // which keeps the loop free of branches
     if constexpr (H == 1) issue_dy(s2, min(t + 2, last));
@@ -282,7 +282,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) read_dy(ds, rb, wn * (TS / 4) + j * 16, s, fd[s][j]);
+      for (int j = 0; j < FN; ++j) read_dy(ds, rb, wn * (TN / 4) + j * 16, s, fd[s][j]);
     __builtin_amdgcn_sched_barrier(0);
     wait_fragments(fd[0]);
     wait_fragments(fd[1]);
@@ -338,31 +338,31 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   if (H == 0) barrier();
 }
 
-template <int TS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TS == 256 ? 2 : 4)))
+template <int TK, int TN>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(TN == 256 ? 2 : 4)))
 void q8_wgrad_kernel(Q8WeightGrad p, TileSplit sp) {
-  constexpr int FM = TS / 32, FN = TS / 64;
-  __shared__ __attribute__((aligned(1024))) char smem[5 * (TS / 128) * kHalfBytes];
+  constexpr int FM = TK / 32, FN = TN / 64;
+  __shared__ __attribute__((aligned(1024))) char smem[(2 * (TK / 128) + 3 * (TN / 128)) * kHalfBytes];
   const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>((p.rows + kStep - 1) / kStep));
-  const int64_t k0 = static_cast<int64_t>(w.a) * TS, n0 = static_cast<int64_t>(w.b) * TS;
+  const int64_t k0 = static_cast<int64_t>(w.a) * TK, n0 = static_cast<int64_t>(w.b) * TN;
   const uint32_t wave = uniform(threadIdx.x >> 6);
   f32x4 acc[FM][FN];
   if (wave < 4)
-    q8_wgrad_tile<TS, 0>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
+    q8_wgrad_tile<TK, TN, 0>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
   else
-    q8_wgrad_tile<TS, 1>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
+    q8_wgrad_tile<TK, TN, 1>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
 
   const int lane = lane_index(), r16 = lane & 15, g4 = lane >> 4;
   const int wm = static_cast<int>(wave >> 2), wn = static_cast<int>(wave & 3);
-  const TileOut o = tile_out(w, TS, p.base, p.out, p.out_dt, p.outs, p.cols, p.ws);
+  const TileOut o = tile_out(w, TK, TN, p.base, p.out, p.out_dt, p.outs, p.cols, p.ws);
   const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int r = wn * (TS / 4) + j * 16 + r16;
+    const int r = wn * (TN / 4) + j * 16 + r16;
     if (r >= o.rows) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int c = wm * (TS / 2) + (v * 4 + g4) * FM;
+      const int c = wm * (TK / 2) + (v * 4 + g4) * FM;
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
@@ -398,10 +398,13 @@ __global__ __launch_bounds__(256) void q8_pad_rows_kernel(const uint16_t *__rest
   }
 }
 
-// Microseconds a step of 64 rows, measured on 8192 rows: 1.5 with one
-// work-group on the chip, 1.6 with 256, a 128-tile 0.76 alone on its CU and
-// 1.12 for two.
-constexpr TileCosts kCosts = {1.5f, 1.6f, 0.76f, 1.12f};
+// Microseconds a step of 64 rows, measured on 4096 and 8192 rows: 256 x 256
+// tiles 1.5 with few work-groups on the chip and 1.6 with 256, 128 x 256 tiles
+// 0.95 and 1.12, 128 x 128 tiles 0.8 alone on their CU and 1.22 for two.  The
+// best with each: 8192 rows, 1024 x 4096 outputs 79 us, 86 and 92; 1500 rows,
+// 3000 x 1800 outputs 44, 34 and 36; 4096 rows, 256 x 1536 outputs 35, 26 and 19.
+constexpr std::initializer_list<TileCost> kCosts = {
+    {256, 256, 1, 1.5f, 1.6f}, {128, 256, 1, 0.95f, 1.12f}, {128, 128, 2, 0.8f, 1.22f}};
 
 // How a weight gradient runs: the tiles' split, and the bytes of its
 // workspace's two parts, the padded dy and the pieces' results.
@@ -446,10 +449,12 @@ hipError_t launch_q8_wgrad(const Q8WeightGrad &args, hipStream_t st) {
   }
   const TileSplit &sp = pl.split;
   const dim3 grid(sp.whole + sp.tail * sp.pieces);
-  if (sp.tile == 256)
-    hipLaunchKernelGGL(q8_wgrad_kernel<256>, grid, dim3(kThreads), 0, st, p, sp);
+  if (sp.ta == 256)
+    hipLaunchKernelGGL((q8_wgrad_kernel<256, 256>), grid, dim3(kThreads), 0, st, p, sp);
+  else if (sp.tb == 256)
+    hipLaunchKernelGGL((q8_wgrad_kernel<128, 256>), grid, dim3(kThreads), 0, st, p, sp);
   else
-    hipLaunchKernelGGL(q8_wgrad_kernel<128>, grid, dim3(kThreads), 0, st, p, sp);
+    hipLaunchKernelGGL((q8_wgrad_kernel<128, 128>), grid, dim3(kThreads), 0, st, p, sp);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || sp.pieces == 1) return e;
   return launch_q8_reduce(static_cast<const float *>(p.ws), sp, p.outs, p.cols, p.base, p.out, p.out_dt, st);
