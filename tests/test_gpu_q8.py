@@ -258,6 +258,28 @@ def test_whole_and_split_tiles():
         check_sum(nsd.q8_weight_grad(dy, z8, dtype=dtype), want, mag, k, dtype)
 
 
+# (128 x 256 tiles: whole, split, and both)
+@pytest.mark.parametrize("t,n,k", [(65, 1846, 2187), (1500, 3001, 1801), (2005, 2723, 403), (1349, 2693, 3005), (1601, 2049, 2051)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("base", ["none", "out"])
+def test_weight_grad_tiles(t, n, k, dtype, base):
+    """Every tile shape of the weight gradient, with ragged edges, against
+    float64 products on the GPU of the values that the codes stand for."""
+    print(f"weight grad tiles {t} {n} {k} {dtype} {base}", flush=True)
+    torch.manual_seed(t)
+    x8 = nsd.q8_quantize(torch.randn(t, k, device="cuda").to(BF16))
+    dy = (0.01 * torch.randn(t, n, device="cuda")).to(BF16)
+    b = (0.05 * torch.randn(n, k, device="cuda")).to(dtype)
+    s = (x8.scales[:, :t].t().to(torch.int64) - 127 + 1023 << 52).view(torch.float64)
+    xv, dv = (x8.codes.double() * s.repeat_interleave(128, 1))[:, :k].contiguous(), dy.double().t().contiguous()
+    want, mag = dv @ xv, dv.abs() @ xv.abs()
+    out = None
+    if base == "out":
+        want, mag, out = want + b.double(), mag + b.double().abs(), b
+    got = nsd.q8_weight_grad(dy, x8, out=out, dtype=dtype, base=out)
+    check_sum(got, want.cpu().numpy(), mag.cpu().numpy(), t + 1, (t, n, k, base))
+
+
 def test_no_rows():
     print("no rows", flush=True)
     rng = np.random.default_rng(1)
