@@ -10,6 +10,11 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(1))) u32x4 g_u32x4;
+// ... at the address of any 2-byte or 4-byte element
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef __attribute__((address_space(1))) u32x4_at2 g_u32x4_at2;
+typedef __attribute__((address_space(1))) u32x4_at4 g_u32x4_at4;
 typedef __attribute__((address_space(1))) u32x2 g_u32x2;
 typedef __attribute__((address_space(1))) f32x4 g_f32x4;
 typedef __attribute__((address_space(1))) uint32_t g_u32;
