@@ -177,8 +177,8 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 
 // ---- tiles: many rows ----
 //
-// One work-group of 8 waves (2 x 4) computes TS x TS outputs, TS outputs of
-// the weight by TS rows; each wave TS/2 x TS/4 in 16 x 16 blocks.  K advances
+// One work-group of 8 waves (2 x 4) computes TA outputs of the weight by TB
+// rows; each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances
 // one 128-code block per step.  Both operand tiles go from global memory into
 // LDS by LDS-bound loads (16 bytes a lane, 128-byte rows, the 16-byte chunk
 // XORed with (row / 2) mod 8, which keeps the fragment reads off each other's
@@ -202,12 +202,12 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 constexpr int kTileThreads = 512;
 constexpr int kRowBytes = 128;
 
-template <int TS, bool EXACT>
+template <int TA, int TB, bool EXACT>
 __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p, int64_t n0, int64_t t0, int kbeg,
-                                        int kend, f32x4 (&acc)[TS / 32][TS / 64]) {
-  constexpr int FM = TS / 32, FN = TS / 64;
-  constexpr int kOperand = TS * kRowBytes, kStage = 2 * kOperand + 256;
-  constexpr int kPerLoader = TS / 64;  // 1 KB loads per wave and half of an operand tile
+                                        int kend, f32x4 (&acc)[TA / 32][TB / 64]) {
+  constexpr int FM = TA / 32, FN = TB / 64;
+  // a stage: the weight's tile, the rows', their scales
+  constexpr int kWeight = TA * kRowBytes, kScales = kWeight + TB * kRowBytes, kStage = kScales + 256;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -218,14 +218,14 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
   const uint8_t *const gb = p.b + n0 * p.kp, *const ga = p.a + t0 * p.kp;
   const uint8_t *const gs = p.sa + t0;
   // the last output and row of the tile that exist, and the last scale word
-  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TS - 1)));
-  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TS - 1)));
-  const uint32_t soff = static_cast<uint32_t>(min(static_cast<int64_t>(4 * (lane % (TS / 4))), t4 - 4 - t0));
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TA - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TB - 1)));
+  const uint32_t soff = static_cast<uint32_t>(min(static_cast<int64_t>(4 * (lane % (TB / 4))), t4 - 4 - t0));
   // loads: lane l of 1 KB load j of a half fills LDS row (j * 4 + wn) * 8 + l / 8,
   // physical chunk l % 8
   const int q = (wn & 1) * 8 + (lane >> 3);
   const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (((wn & 1) * 4 + (lane >> 4)) & 7)) * 16;
-  const int base_n = ((q & 3) * 4 + (q >> 2)) * FM + (wn >> 1) + wm * (TS / 2);
+  const int base_n = ((q & 3) * 4 + (q >> 2)) * FM + (wn >> 1) + wm * (TA / 2);
   const int base_t = q * FN + (wn >> 1);
   auto issue = [&](int slot, int kb) {
     lds_char *const st = lds + slot * kStage;
@@ -240,20 +240,20 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
     // live across the loop
     asm volatile("" : "+v"(bn), "+v"(bt));
 #pragma unroll
-    for (int j = 0; j < kPerLoader; ++j) load(bb, min(bn + 2 * j, lim_n), wm * (kOperand / 2) + j * 4096);
+    for (int j = 0; j < TA / 64; ++j) load(bb, min(bn + 2 * j, lim_n), wm * (kWeight / 2) + j * 4096);
     if (wm == 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < kPerLoader; ++j) {
-          // row s of the tile's LDS rows: quarter s / (TS / 4), then block and column
-          const int s = h * (TS / 2) + j * 32, in_quarter = s % (TS / 4);
-          const int row = s / (TS / 4) * (TS / 4) + in_quarter / 16;
-          load(ba, min(bt + row, lim_t), kOperand + h * (kOperand / 2) + j * 4096);
+        for (int j = 0; j < TB / 64; ++j) {
+          // row s of the tile's LDS rows: quarter s / (TB / 4), then block and column
+          const int s = h * (TB / 2) + j * 32, in_quarter = s % (TB / 4);
+          const int row = s / (TB / 4) * (TB / 4) + in_quarter / 16;
+          load(ba, min(bt + row, lim_t), kWeight + s * kRowBytes);
         }
       if (wn == 0)
         __builtin_amdgcn_global_load_lds((const void *)(gs + kb * t4 + soff),
-                                         (__attribute__((address_space(3))) void *)(st + 2 * kOperand), 4, 0, 0);
+                                         (__attribute__((address_space(3))) void *)(st + kScales), 4, 0, 0);
     }
   };
 
@@ -263,11 +263,11 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // this wave's block of the weight's scales: one byte per step
-  const int64_t nb = (n0 + wm * (TS / 2)) / kQ8Block, last_nb = (p.outs - 1) / kQ8Block;
+  const int64_t nb = (n0 + wm * (TA / 2)) / kQ8Block, last_nb = (p.outs - 1) / kQ8Block;
   const uint8_t *const sb = p.sb + min(nb, last_nb) * nkb;
   auto row_scales = [&](const lds_char *st) -> uint32_t {
-    if constexpr (FN == 4) return *(const lds_u32 *)(st + 2 * kOperand + wn * 64 + r16 * 4);
-    return *(const lds_u16 *)(st + 2 * kOperand + wn * 32 + r16 * 2);
+    if constexpr (FN == 4) return *(const lds_u32 *)(st + kScales + wn * 64 + r16 * 4);
+    return *(const lds_u16 *)(st + kScales + wn * 32 + r16 * 2);
   };
   // 16 bytes (chunk sub * 4 + g4) of row r16 of 16-row block i of an operand;
   // the swizzle is the same in every block
@@ -281,7 +281,7 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
   if (wm == 1) barrier();
   for (int kb = kbeg; kb < kend; ++kb) {
     const lds_char *const st = lds + (kb & 1) * kStage;
-    const lds_char *const opb = st + wm * (kOperand / 2), *const opa = st + kOperand + wn * (kOperand / 4);
+    const lds_char *const opb = st + wm * (kWeight / 2), *const opa = st + kWeight + wn * (TB / 4 * kRowBytes);
     // the last step loads its own block again, into the free stage, which
     // keeps the loop free of a branch
     issue((kb + 1) & 1, min(kb + 1, kend - 1));
@@ -369,27 +369,27 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
   if (wm == 0) barrier();
 }
 
-template <int TS, bool EXACT>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TS == 256 ? 2 : 4)))
+template <int TA, int TB, bool EXACT>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TB == 256 ? 2 : 4)))
 void q8_tile_kernel(Q8Product p, TileSplit sp) {
-  constexpr int FM = TS / 32, FN = TS / 64;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * (2 * TS * kRowBytes + 256)];
+  constexpr int FM = TA / 32, FN = TB / 64;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * ((TA + TB) * kRowBytes + 256)];
   const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ8Block));
-  const int64_t n0 = static_cast<int64_t>(w.a) * TS, t0 = static_cast<int64_t>(w.b) * TS;
+  const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
   f32x4 acc[FM][FN];
-  q8_tile<TS, EXACT>((lds_char *)smem, p, n0, t0, w.begin, w.end, acc);
+  q8_tile<TA, TB, EXACT>((lds_char *)smem, p, n0, t0, w.begin, w.end, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
-  const TileOut o = tile_out(w, TS, TS, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
+  const TileOut o = tile_out(w, TA, TB, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
   const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int r = wn * (TS / 4) + r16 * FN + j;
+    const int r = wn * (TB / 4) + r16 * FN + j;
     if (r >= o.rows) continue;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int c = wm * (TS / 2) + (v * 4 + g4) * FM;
+      const int c = wm * (TA / 2) + (v * 4 + g4) * FM;
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
@@ -402,12 +402,16 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
 
 namespace {
 
-// Microseconds a step of one K block, measured on 80 .. 4096 rows: bf16, 1.03
-// with one work-group on the chip and 1.5 with 256 (the clock gives way), a
-// 128-tile 0.6 alone on its CU and 1.06 for two; fp32 results 2.23 and 2.9,
-// 0.94 and 1.88.
-constexpr std::initializer_list<TileCost> kBf16Costs = {{256, 256, 1, 1.03f, 1.5f}, {128, 128, 2, 0.6f, 1.06f}},
-                                          kExactCosts = {{256, 256, 1, 2.23f, 2.9f}, {128, 128, 2, 0.95f, 1.88f}};
+// Microseconds a step of one K block, measured on 80 .. 8192 rows.  bf16: 256 x
+// 256 tiles 1.03 with one work-group on the chip and 1.5 with 256 (the clock
+// gives way), 128 x 256 tiles 0.8 and 0.97, 128 x 128 tiles 0.6 alone on their
+// CU and 1.06 for two.  The best with each: 2048 rows of a 4096 x 8192 weight 73
+// us, 65.5 and 71; 1024 rows of a 4096 x 4096 one 38, 31 and 26; 4096 rows 56, 73
+// and 76.  fp32 results of the first: 117, 112 and 127.
+constexpr std::initializer_list<TileCost> kBf16Costs = {
+    {256, 256, 1, 1.03f, 1.5f}, {128, 256, 1, 0.8f, 0.97f}, {128, 128, 2, 0.6f, 1.06f}};
+constexpr std::initializer_list<TileCost> kExactCosts = {
+    {256, 256, 1, 2.23f, 2.9f}, {128, 256, 1, 1.38f, 1.68f}, {128, 128, 2, 0.95f, 1.88f}};
 
 // How a product runs: streamed (row blocks and waves of a work-group) or in
 // tiles.
@@ -456,13 +460,13 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
   return pl;
 }
 
-template <int TS>
+template <int TA, int TB>
 hipError_t launch_tiles(const Q8Product &p, const TileSplit &sp, hipStream_t st) {
   const dim3 grid(sp.whole + sp.tail * sp.pieces);
   if (p.out_dt == kF32)
-    hipLaunchKernelGGL((q8_tile_kernel<TS, true>), grid, dim3(kTileThreads), 0, st, p, sp);
+    hipLaunchKernelGGL((q8_tile_kernel<TA, TB, true>), grid, dim3(kTileThreads), 0, st, p, sp);
   else
-    hipLaunchKernelGGL((q8_tile_kernel<TS, false>), grid, dim3(kTileThreads), 0, st, p, sp);
+    hipLaunchKernelGGL((q8_tile_kernel<TA, TB, false>), grid, dim3(kTileThreads), 0, st, p, sp);
   return hipGetLastError();
 }
 
@@ -492,7 +496,9 @@ hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
   if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, pl.nn, st) : launch_stream<1, 4>(p, pl.nn, st);
   if (pl.nt == 2) return launch_stream<2, 4>(p, pl.nn, st);
   if (pl.nt == 4) return launch_stream<4, 4>(p, pl.nn, st);
-  const hipError_t e = pl.split.ta == 256 ? launch_tiles<256>(p, pl.split, st) : launch_tiles<128>(p, pl.split, st);
+  const hipError_t e = pl.split.ta == 256   ? launch_tiles<256, 256>(p, pl.split, st)
+                       : pl.split.tb == 256 ? launch_tiles<128, 256>(p, pl.split, st)
+                                            : launch_tiles<128, 128>(p, pl.split, st);
   if (e != hipSuccess || pl.split.pieces == 1) return e;
   return launch_q8_reduce(p.ws, pl.split, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
 }

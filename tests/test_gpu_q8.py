@@ -203,6 +203,28 @@ def test_product_of_small_integers(t, n, k, dtype):
     assert np.array_equal(got, want), np.argwhere(got != want)[:5]
 
 
+# (128 x 256 tiles: whole, split, both; 256 x 256 tiles)
+@pytest.mark.parametrize("t,n,k", [(1505, 2801, 131), (1500, 1000, 9001), (2230, 3602, 903), (2309, 3424, 133)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_tiles(t, n, k, transpose, dtype):
+    """Every tile shape of the product, with ragged edges, against float64
+    products on the GPU of the values that the codes stand for."""
+    print(f"product tiles {t} {n} {k} {transpose} {dtype}", flush=True)
+    torch.manual_seed(t)
+    x8 = nsd.q8_quantize(torch.randn(t, k, device="cuda").to(BF16))
+    w = (0.02 * torch.randn(n, k, device="cuda")).to(BF16)
+    w8 = nsd.q8_quantize_weights([w.t().contiguous() if transpose else w])[0]
+    codes, scales = (w8.codes_t, w8.scales_t) if transpose else (w8.codes, w8.scales)
+    power = lambda b: (b.to(torch.int64) - 127 + 1023 << 52).view(torch.float64)  # noqa: E731
+    xv = (x8.codes.double() * power(x8.scales[:, :t].t()).repeat_interleave(128, 1))[:, :k]
+    wv = (codes.double() * power(scales).repeat_interleave(128, 0)[:n].repeat_interleave(128, 1))[:, :k]
+    wv = wv.t().contiguous()
+    got = nsd.q8_matmul(x8, w8, transpose=transpose, dtype=dtype)
+    check_sum(got, (xv @ wv).cpu().numpy(), (xv.abs() @ wv.abs()).cpu().numpy(), k, (t, n, k),
+              CUT if dtype == BF16 else 0.0)
+
+
 WGRAD_SIZES = [(1, 1, 1), (1, 128, 128), (2, 300, 513), (3, 17, 130), (31, 64, 64), (32, 65, 129), (33, 256, 256),
                (64, 257, 200), (65, 40, 1000), (127, 1001, 33), (200, 136, 384), (333, 520, 513), (1000, 129, 257),
                (1025, 256, 512), (2100, 8, 128),
