@@ -13,8 +13,12 @@ typedef __attribute__((address_space(1))) u32x4 g_u32x4;
 // ... at the address of any 2-byte or 4-byte element
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 typedef __attribute__((address_space(1))) u32x4_at2 g_u32x4_at2;
 typedef __attribute__((address_space(1))) u32x4_at4 g_u32x4_at4;
+typedef __attribute__((address_space(1))) u32x2_at2 g_u32x2_at2;
+typedef __attribute__((address_space(1))) f32x4_at4 g_f32x4_at4;
 typedef __attribute__((address_space(1))) u32x2 g_u32x2;
 typedef __attribute__((address_space(1))) f32x4 g_f32x4;
 typedef __attribute__((address_space(1))) uint32_t g_u32;
@@ -107,29 +111,29 @@ __device__ __forceinline__ TileOut tile_out(const TileWork &w, int ta, int tb, c
 }
 
 // N (4 or 8) consecutive outputs, plus base where there is one; `left` of them
-// exist.  vec: their addresses are aligned to the vector (16 bytes, or 8 for
-// four bf16).  base may be out.
+// exist.  Vector accesses at any element's address (8192 rows x 4095 bf16 outputs
+// of 512 codes each: 34 us, element by element 83); base may be out.
 template <int N>
-__device__ __forceinline__ void finish_run(const void *base, void *out, int32_t dt, int64_t at, int64_t left, bool vec,
+__device__ __forceinline__ void finish_run(const void *base, void *out, int32_t dt, int64_t at, int64_t left,
                                            float (&v)[N]) {
-  if (vec && left >= N) {
+  if (left >= N) {
     if (dt == kF32) {
       if (base) {
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {
-          const f32x4 b = *(const g_f32x4 *)(static_cast<const float *>(base) + at + 4 * h);
+          const f32x4 b = *(const g_f32x4_at4 *)(static_cast<const float *>(base) + at + 4 * h);
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[4 * h + k] += b[k];
         }
       }
 #pragma unroll
       for (int h = 0; h < N / 4; ++h)
-        *(g_f32x4 *)(static_cast<float *>(out) + at + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        *(g_f32x4_at4 *)(static_cast<float *>(out) + at + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
     } else {
       if (base) {
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {
-          const u32x2 b = *(const g_u32x2 *)(static_cast<const uint16_t *>(base) + at + 4 * h);
+          const u32x2 b = *(const g_u32x2_at2 *)(static_cast<const uint16_t *>(base) + at + 4 * h);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             v[4 * h + 2 * k] += __uint_as_float(b[k] << 16);
@@ -143,9 +147,9 @@ __device__ __forceinline__ void finish_run(const void *base, void *out, int32_t 
         u[k] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k])) |
                (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k + 1])) << 16);
       if constexpr (N == 8)
-        *(g_u32x4 *)(static_cast<uint16_t *>(out) + at) = u32x4{u[0], u[1], u[2], u[3]};
+        *(g_u32x4_at2 *)(static_cast<uint16_t *>(out) + at) = u32x4{u[0], u[1], u[2], u[3]};
       else
-        *(g_u32x2 *)(static_cast<uint16_t *>(out) + at) = u32x2{u[0], u[1]};
+        *(g_u32x2_at2 *)(static_cast<uint16_t *>(out) + at) = u32x2{u[0], u[1]};
     }
   } else {
 #pragma unroll

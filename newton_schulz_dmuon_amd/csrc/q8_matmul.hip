@@ -171,7 +171,7 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
     const int64_t t = t0 + r16 * NT + at % NT, n = n0 + at / NT * 16 + 4 * g4;
     if (t >= p.rows) continue;
     float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, p.outs % 4 == 0, v);
+    finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
   }
 }
 
@@ -382,7 +382,6 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
   const TileOut o = tile_out(w, TA, TB, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
-  const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int r = wn * (TB / 4) + r16 * FN + j;
@@ -393,7 +392,7 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
-      finish_run<FM>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, vec, run);
+      finish_run<FM>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
   }
 }

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void q8_reduce_kernel(const float *__restrict_
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[4 * h + k] += w[k];
     }
-  finish_run<8>(base, out, dt, r * cols + c, cols - c, cols % (dt == kF32 ? 4 : 8) == 0, v);
+  finish_run<8>(base, out, dt, r * cols + c, cols - c, v);
 }
 
 }  // namespace

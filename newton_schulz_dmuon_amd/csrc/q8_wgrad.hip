@@ -360,7 +360,6 @@ void q8_wgrad_kernel(Q8WeightGrad p, TileSplit sp) {
   const int lane = lane_index(), r16 = lane & 15, g4 = lane >> 4;
   const int wm = static_cast<int>(wave >> 2), wn = static_cast<int>(wave & 3);
   const TileOut o = tile_out(w, TK, TN, p.base, p.out, p.out_dt, p.outs, p.cols, p.ws);
-  const bool vec = o.ld % (FM == 8 && o.dt != kF32 ? 8 : 4) == 0;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int r = wn * (TN / 4) + j * 16 + r16;
@@ -371,7 +370,7 @@ void q8_wgrad_kernel(Q8WeightGrad p, TileSplit sp) {
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
-      finish_run<FM>(o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, vec, run);
+      finish_run<FM>(o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
   }
 }
@@ -385,7 +384,7 @@ __global__ __launch_bounds__(256) void q8_wgrad_empty_kernel(Q8WeightGrad p) {
   const int64_t n = p.outs * p.cols;
   for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; at < n; at += gridDim.x * int64_t(2048)) {
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    finish_run<8>(p.base, p.out, p.out_dt, at, n - at, true, v);
+    finish_run<8>(p.base, p.out, p.out_dt, at, n - at, v);
   }
 }
 
