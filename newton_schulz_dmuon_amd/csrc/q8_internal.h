@@ -1,7 +1,6 @@
 // Declarations shared by the 8-bit block products' entry points (q8_api.cpp)
-// and kernels (q8_quant.hip, q8_matmul.hip, q8_wgrad.hip,
-// q8_reduce.hip).  Not part of the
-// C ABI.
+// and kernels (q8_quant.hip, q8_matmul.hip, q8_wgrad.hip, q8_reduce.hip).  Not
+// part of the C ABI.
 #pragma once
 
 #include <initializer_list>

@@ -195,10 +195,10 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 // r * FN + j, so that a lane's FN scale bytes are one LDS word.
 //
 // Bound by the matrix cores at the clock they leave: 8192 rows of a 14336 x
-// 4096 weight take 376 us, 2.56 PFLOP/s (dense peak 5, which the clock under
-// load does not allow; a library 8-bit product with one scale 2.5).  fp32 results, which
-// multiply in bf16 and expand in the same phase, 2001 rows by a transposed
-// 18944 x 3584 weight: 209 us, 1.30 PFLOP/s (a library bf16 product 1.38).
+// 4096 weight take 351 to 379 us, 2.54 to 2.74 PFLOP/s (a library 8-bit product
+// with one scale 2.5).  fp32 results, which multiply in bf16 and expand in the
+// same phase, 2001 rows by a transposed 18944 x 3584 weight: 210 to 215 us, 1.3
+// PFLOP/s (a library bf16 product 1.38).
 constexpr int kTileThreads = 512;
 constexpr int kRowBytes = 128;
 

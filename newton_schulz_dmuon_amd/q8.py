@@ -15,6 +15,14 @@ A training step of one linear layer::
     dx = nsd.q8_matmul(nsd.q8_quantize(dy), w8, transpose=True)   # dy w
     nsd.q8_weight_grad(dy, x8, out=grad)             # dy^T x
     nsd.muon_step([w], [grad], [momentum], [scale])
+
+The functions enqueue kernels on ``stream`` (the current one by default) and
+record no gradients: the backward pass is the last two calls.  Results that are
+not passed in are new tensors; without ``workspace`` a call that needs scratch
+allocates it.  A ``Workspace`` serves any number of calls on one stream; work
+that may overlap (calls on two streams, a call and a replayed graph, two graphs)
+needs one each.  Every call can be captured into a graph, and the same call
+gives the same bits.
 """
 
 from __future__ import annotations
