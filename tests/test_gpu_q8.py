@@ -574,6 +574,39 @@ def test_another_stream(t):
     del junk
 
 
+@pytest.mark.parametrize("own_workspaces", [False, True])
+def test_two_streams_at_once(own_workspaces):
+    """Calls in flight on two streams, and a graph replaying beside them, give
+    the results of calls one after the other."""
+    print(f"two streams {own_workspaces}", flush=True)
+    sizes = (300, 2048)
+    inputs = [layer_inputs(20 + i, t) for i, t in enumerate(sizes)]
+    want = []
+    for x, dy, w, g in inputs:
+        g = g.clone()
+        want.append(layer(x, dy, w, g) + (g,))
+    ws = [nsd.Workspace() if own_workspaces else None for _ in range(3)]
+    x, dy, w, g0 = inputs[1]
+    gg = g0.clone()
+    layer(x, dy, w, gg, workspace=ws[2])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = layer(x, dy, w, gg, workspace=ws[2])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        gg.copy_(g0)
+        grads = [i[3].clone() for i in inputs]
+        torch.cuda.synchronize()
+        graph.replay()
+        got = [layer(*i[:3], g, stream=s, workspace=v) for i, g, s, v in zip(inputs, grads, streams, ws)]
+        torch.cuda.synchronize()
+        for a, g, b in zip(got, grads, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(g, b[2])
+        assert torch.equal(captured[0], want[1][0]) and torch.equal(captured[1], want[1][1])
+        assert torch.equal(gg, want[1][2])
+
+
 @pytest.mark.parametrize("t", [1, 40, 300, 2048])
 def test_graph_replays(t):
     """Captured with a workspace of its own and replayed on changing inputs,
