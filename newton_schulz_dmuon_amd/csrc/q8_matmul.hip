@@ -86,8 +86,8 @@ __device__ __forceinline__ int uniform_scale(const uint8_t *p) {
 // The rows' codes come from L2, once per 16 NN outputs.  Each wave keeps kAhead
 // blocks' loads in flight; the waves' sums are added through LDS in wave order.
 // Rows and outputs behind the last are clamped for the loads and not stored.
-// One row of a 14336 x 4096 weight takes 13.9 us, 4.2 TB/s (HBM); 24 rows of a
-// 4096 x 14336 one 19.0 us, where the rows' codes make up the larger part of
+// One row of a 14336 x 4096 weight takes 13.4 us, 4.4 TB/s (HBM); 24 rows of a
+// 4096 x 14336 one 18.6 us, where the rows' codes make up the larger part of
 // the 33 GB/s that a CU takes in.
 // Column r of row block j is row r * NT + j, so that a lane's NT scale bytes
 // are one load.
@@ -140,8 +140,13 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
         acc[i][j] =
             block_product<EXACT>(fb[u][i], wb[u], fa[u][j], static_cast<int>((wa[u] >> (8 * j)) & 0xff), acc[i][j]);
   };
+  // in the loop's order, or its waits would be for all of them at every turn (128
+  // rows of a 4096 x 4096 weight: 15.0 us so, 14.1 in order)
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, wave + u * WAVES);
+  for (int u = 0; u < kAhead; ++u) {
+    load(u, wave + u * WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // each block's registers take the block kAhead further on as soon as it has
   // been multiplied; the last kAhead blocks load nothing more
   int k0 = wave;
@@ -195,9 +200,9 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 // r * FN + j, so that a lane's FN scale bytes are one LDS word.
 //
 // Bound by the matrix cores at the clock they leave: 8192 rows of a 14336 x
-// 4096 weight take 351 to 379 us, 2.54 to 2.74 PFLOP/s (a library 8-bit product
+// 4096 weight take 351 to 381 us, 2.53 to 2.74 PFLOP/s (a library 8-bit product
 // with one scale 2.5).  fp32 results, which multiply in bf16 and expand in the
-// same phase, 2001 rows by a transposed 18944 x 3584 weight: 210 to 215 us, 1.3
+// same phase, 2001 rows by a transposed 18944 x 3584 weight: 210 to 218 us, 1.3
 // PFLOP/s (a library bf16 product 1.38).
 constexpr int kTileThreads = 512;
 constexpr int kRowBytes = 128;

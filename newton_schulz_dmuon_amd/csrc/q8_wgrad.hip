@@ -9,7 +9,7 @@
 // gradient; sums are fp32.
 //
 // Bound by LDS reads and the matrix cores in turn: 8192 rows, 14336 x 4096
-// outputs, take 766 to 809 us, 1.2 PFLOP/s (a library bf16 product of that size
+// outputs, take 766 to 815 us, 1.2 PFLOP/s (a library bf16 product of that size
 // 1.38).  With few outputs the fp32 pieces and the reduce launch add to it:
 // 4096 rows, 1024 x 4096 outputs, 53 us.
 
