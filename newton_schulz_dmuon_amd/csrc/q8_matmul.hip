@@ -78,6 +78,11 @@ __device__ __forceinline__ int uniform_scale(const uint8_t *p) {
   return static_cast<int>((w >> ((at & 3) * 8)) & 0xff);
 }
 
+// K blocks in flight a wave of the streaming kernel.
+constexpr int stream_ahead(int nt, int nn, int waves) {
+  return waves == 8 ? 2 : nt * nn > 2 ? 2 : 3;
+}
+
 // ---- few rows: the weight's bytes ----
 //
 // A work-group takes 16 NN outputs of up to 16 NT rows, its WAVES waves every
@@ -93,8 +98,10 @@ __device__ __forceinline__ int uniform_scale(const uint8_t *p) {
 // are one load.
 template <int NT, int NN, int WAVES, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
-  constexpr int kAhead = NT * NN > 2 ? 2 : 4;
-  __shared__ f32x4 part[WAVES][NT * NN][64];
+  constexpr int kAhead = stream_ahead(NT, NN, WAVES);
+  constexpr int kBlock = 16 * kQ8Block, kScales = (NN + NT) * kBlock, kStage = kScales + 256;
+  constexpr int kLoads = 2 * (NN + NT) + 1;  // vector loads a K block
+  __shared__ __attribute__((aligned(1024))) char smem[WAVES * kAhead * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
@@ -102,78 +109,123 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
   const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * (16 * NT);
   const int nkb = static_cast<int>(p.kp / kQ8Block);
   const int64_t t4 = (p.rows + 3) & ~static_cast<int64_t>(3);
-  const uint8_t *a[NT], *b[NN];
+  lds_char *const ring = (lds_char *)smem + wave * (kAhead * kStage);
+  // lane l of 1 KB load h of a block fills LDS row 8 h + l / 8, physical chunk l % 8
+  const uint8_t *const gb = p.b + n0 * p.kp, *const ga = p.a + t0 * p.kp;
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(16 * NN - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(16 * NT - 1)));
+  uint32_t ob[NN][2], oa[NT][2];
 #pragma unroll
-  for (int i = 0; i < NN; ++i) b[i] = p.b + min(n0 + i * 16 + r16, p.outs - 1) * p.kp + g4 * 16;
+  for (int h = 0; h < 2; ++h) {
+    const int row = 8 * h + (lane >> 3);
+    const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (row >> 1)) * 16;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) a[j] = p.a + min(t0 + r16 * NT + j, p.rows - 1) * p.kp + g4 * 16;
-  const uint8_t *const sa = p.sa + min(t0 + r16 * NT, t4 - NT);
-  const uint8_t *const sb = p.sb + n0 / kQ8Block * nkb;  // 16 NN divides 128
+    for (int i = 0; i < NN; ++i)
+      ob[i][h] = __umul24(static_cast<uint32_t>(min(i * 16 + row, lim_n)), static_cast<uint32_t>(p.kp)) + chunk;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      oa[j][h] = __umul24(static_cast<uint32_t>(min(row * NT + j, lim_t)), static_cast<uint32_t>(p.kp)) + chunk;
+  }
+  // the scales of a stage: half a wave loads the rows' words, half the word with
+  // the weight's byte (16 NN divides 128)
+  const uint8_t *const sb = p.sb + n0 / kQ8Block * nkb;
+  const uintptr_t scale0 = lane < 32 ? reinterpret_cast<uintptr_t>(p.sa + t0 + min(static_cast<int64_t>(4 * lane), t4 - 4 - t0))
+                                     : reinterpret_cast<uintptr_t>(sb);
+  const int64_t scale_step = lane < 32 ? t4 : 1;
   f32x4 acc[NN][NT];
 #pragma unroll
   for (int i = 0; i < NN; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x8 fb[kAhead][NN], fa[kAhead][NT];
-  uint32_t wa[kAhead];
-  int wb[kAhead];
   auto load = [&](int u, int block) {
     const int kb = min(block, nkb - 1);
+    lds_char *const st = ring + u * kStage;
+    auto piece = [&](const uint8_t *src, int at) {
+      __builtin_amdgcn_global_load_lds((const void *)src, (__attribute__((address_space(3))) void *)(st + at), 16, 0, 0);
+    };
+    const uint8_t *const bb = gb + static_cast<int64_t>(kb) * kQ8Block, *const ba = ga + static_cast<int64_t>(kb) * kQ8Block;
 #pragma unroll
-    for (int i = 0; i < NN; ++i) fb[u][i] = load32(b[i] + static_cast<int64_t>(kb) * kQ8Block);
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fa[u][j] = load32(a[j] + static_cast<int64_t>(kb) * kQ8Block);
-    const uint8_t *const s = sa + kb * t4;
-    if constexpr (NT == 4)
-      wa[u] = *(const g_u32 *)s;
-    else if constexpr (NT == 2)
-      wa[u] = *(const g_u16 *)s;
-    else
-      wa[u] = *(const g_u8 *)s;
-    wb[u] = uniform_scale(sb + kb);
+      for (int i = 0; i < NN; ++i) piece(bb + ob[i][h], i * kBlock + h * 1024);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) piece(ba + oa[j][h], (NN + j) * kBlock + h * 1024);
+    }
+    __builtin_amdgcn_global_load_lds((const void *)((scale0 + kb * scale_step) & ~static_cast<uintptr_t>(3)),
+                                     (__attribute__((address_space(3))) void *)(st + kScales), 4, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  auto multiply = [&](int u) {
+  // a lane's 32 codes of row r16 of a block: chunks g4 and g4 + 4
+  const uint32_t at = static_cast<uint32_t>(r16 * kQ8Block + ((g4 ^ (r16 >> 1)) & 7) * 16);
+  i32x8 fb[NN], fa[NT];
+  uint32_t wa;
+  int wb;
+  auto read = [&](int u, int kb) {
+    const lds_char *const st = ring + u * kStage;
+    auto codes = [&](const lds_char *b) {
+      const u32x4 lo = *(const lds_u32x4 *)(b + at), hi = *(const lds_u32x4 *)(b + (at ^ 64));
+      return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+                   static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+    };
+#pragma unroll
+    for (int i = 0; i < NN; ++i) fb[i] = codes(st + i * kBlock);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fa[j] = codes(st + (NN + j) * kBlock);
+    if constexpr (NT == 4)
+      wa = *(const lds_u32 *)(st + kScales + r16 * 4);
+    else if constexpr (NT == 2)
+      wa = *(const lds_u16 *)(st + kScales + r16 * 2);
+    else
+      wa = *(const lds_u8 *)(st + kScales + r16);
+    wb = *(const lds_u8 *)(st + kScales + 128 + (reinterpret_cast<uintptr_t>(sb + kb) & 3));
+    // all are in registers before the stage is loaded again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int i = 0; i < NN; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        acc[i][j] =
-            block_product<EXACT>(fb[u][i], wb[u], fa[u][j], static_cast<int>((wa[u] >> (8 * j)) & 0xff), acc[i][j]);
-  };
-  // in the loop's order, or its waits would be for all of them at every turn (128
-  // rows of a 4096 x 4096 weight: 15.0 us so, 14.1 in order)
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    load(u, wave + u * WAVES);
+        acc[i][j] = block_product<EXACT>(fb[i], wb, fa[j], static_cast<int>((wa >> (8 * j)) & 0xff), acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
-  }
-  // each block's registers take the block kAhead further on as soon as it has
-  // been multiplied; the last kAhead blocks load nothing more
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, wave + u * WAVES);
+  // each stage takes the block kAhead further on as soon as its codes have been
+  // read; the last kAhead blocks load nothing more
   int k0 = wave;
   for (; k0 + WAVES * kAhead < nkb; k0 += WAVES * kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      multiply(u);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+      read(u, k0 + u * WAVES);
       load(u, k0 + (kAhead + u) * WAVES);
-      __builtin_amdgcn_sched_barrier(0);
+      multiply();
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (k0 + u * WAVES < nkb) multiply(u);
+    if (k0 + u * WAVES < nkb) {
+      read(u, k0 + u * WAVES);
+      multiply();
+    }
+  // the waves' sums, each in its own part of the ring
+  auto part = [&](int w, int b) { return (lds_f32x4 *)((lds_char *)smem + w * (kAhead * kStage) + b * 1024 + lane * 16); };
 #pragma unroll
   for (int i = 0; i < NN; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+    for (int j = 0; j < NT; ++j) *part(wave, i * NT + j) = acc[i][j];
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < (NN * NT + WAVES - 1) / WAVES; ++q) {
-    const int at = q * WAVES + wave;
-    if (at >= NN * NT) return;
-    f32x4 sum = part[0][at][lane];
+    const int b = q * WAVES + wave;
+    if (b >= NN * NT) return;
+    f32x4 sum = *part(0, b);
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += part[w][at][lane];
-    const int64_t t = t0 + r16 * NT + at % NT, n = n0 + at / NT * 16 + 4 * g4;
+    for (int w = 1; w < WAVES; ++w) sum += *part(w, b);
+    const int64_t t = t0 + r16 * NT + b % NT, n = n0 + b / NT * 16 + 4 * g4;
     if (t >= p.rows) continue;
     float v[4] = {sum[0], sum[1], sum[2], sum[3]};
     finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
