@@ -34,14 +34,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// One lane's share of a row's block: 16 codes of each half of the block, so
-// that the four lanes of a row read 64 consecutive bytes at a time.
-__device__ __forceinline__ i32x8 load32(const uint8_t *p) {
-  const u32x4 lo = *(const g_u32x4 *)p, hi = *(const g_u32x4 *)(p + 64);
-  return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
-               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
-}
-
 // 2^(byte - 127) as fp32, for a scale byte of the format.
 __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
 
@@ -78,24 +70,23 @@ __device__ __forceinline__ int uniform_scale(const uint8_t *p) {
   return static_cast<int>((w >> ((at & 3) * 8)) & 0xff);
 }
 
-// K blocks in flight a wave of the streaming kernel.
-constexpr int stream_ahead(int nt, int nn, int waves) {
-  return waves == 8 ? 2 : nt * nn > 2 ? 2 : 3;
-}
+// K blocks in flight a wave of the streaming kernel: 50 to 100 KB a work-group.
+constexpr int stream_ahead(int nt, int nn, int waves) { return waves == 8 || nt * nn > 2 ? 2 : 3; }
 
 // ---- few rows: the weight's bytes ----
 //
 // A work-group takes 16 NN outputs of up to 16 NT rows, its WAVES waves every
-// WAVES-th K block: together they stream whole runs of the weight's rows, each
-// byte of which is read once, straight into registers (no other wave wants it).
-// The rows' codes come from L2, once per 16 NN outputs.  Each wave keeps kAhead
-// blocks' loads in flight; the waves' sums are added through LDS in wave order.
-// Rows and outputs behind the last are clamped for the loads and not stored.
-// One row of a 14336 x 4096 weight takes 13.4 us, 4.4 TB/s (HBM); 24 rows of a
-// 4096 x 14336 one 18.6 us, where the rows' codes make up the larger part of
-// the 33 GB/s that a CU takes in.
-// Column r of row block j is row r * NT + j, so that a lane's NT scale bytes
-// are one load.
+// WAVES-th K block; the waves' sums are added through LDS in wave order.  Each
+// wave has a ring of stages of its own in LDS, and no barrier: it waits for its
+// own loads.  A block comes by LDS-bound loads of eight whole rows' 128 bytes,
+// the 16-byte chunks XORed with (row / 2) mod 8 against bank conflicts.  (In
+// registers, where each lane loads its row's share, 16 rows to an instruction, a
+// CU took in 33 GB/s; so it is 53: 24 rows of a 4096 x 14336 weight 21.5 and 15.5
+// us, 128 rows of a 4096 x 4096 one 14.1 and 7.9.)  The weight's bytes are read
+// once, the rows' from L2 once per 16 NN outputs.  Rows and outputs behind the
+// last are clamped for the loads and not stored.  Column r of row block j is row
+// r * NT + j, so that a lane's NT scale bytes are one LDS word.
+// One row of a 14336 x 4096 weight takes 13.5 us, 4.4 TB/s (HBM).
 template <int NT, int NN, int WAVES, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
   constexpr int kAhead = stream_ahead(NT, NN, WAVES);
@@ -476,20 +467,21 @@ struct Plan {
   TileSplit split;
 };
 
-// The streaming kernel's time in microseconds, as measured (rows 1 .. 128 of
-// weights 1024 x 4096 to 18944 x 3584, within 15%): a work-group takes in its
-// weight and row codes at 33 GB/s, 256 of them at a time, or the weight comes
-// from memory at 4.9 TB/s, whichever is longer.  64 rows of a 14336 x 4096
-// weight: 26 us with 4 x 2 blocks a work-group, 54 with one; of a 1024 x 4096
-// weight: 14 and 6.1.
+// The streaming kernel's time in microseconds, as measured (rows 1 .. 512 of
+// weights 256 x 1536 to 18944 x 3584): a work-group takes in its weight and row
+// codes at 53 GB/s, 256 of them at a time, while the weight comes from memory at
+// 4.9 TB/s; a quarter of the shorter of the two does not hide.  64 rows of a
+// 14336 x 4096 weight: 21 us with 4 x 2 blocks a work-group, 39 with one, 25 in
+// tiles; of a 4096 x 14336 one: 20.5 with 2 x 2, 36 and 24.
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
   const float bytes = static_cast<float>((16 * nn + std::min<int64_t>(16 * nt, rows)) * kp);
-  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 33e3f;
-  return 3.f + std::max(taken, static_cast<float>(outs * kp) / 4.9e6f);
+  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
+  const float memory = static_cast<float>(outs * kp) / 4.9e6f;
+  return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
 }
-// Rows up to which it is considered: 512 rows of a 256 x 1536 weight still take
-// 4.8 us against 10.0 in tiles, of a 1024 x 4096 one 14.5 against 16.7.
+// Rows up to which it is considered: 512 rows of a 256 x 1536 weight take 3.2 us
+// against 10.0 in tiles, of a 1024 x 4096 one 7.9 against 16.6.
 constexpr int64_t kStreamRows = 1024;
 
 Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
@@ -506,11 +498,11 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
       pl.nt = nt;
       pl.nn = nn;
     }
-  // Eight waves share K where it is long and a work-group has one row block
-  // (one row, 4096 x 4096: 5.7 us against 6.2 with four), else four (24 rows,
-  // 4096 x 14336: 20.5 against 22.1; 16 rows, 256 x 1536: 3.8 against 5.5).
+  // Eight waves share a long K where a work-group has one block of each (one row,
+  // 4096 x 14336: 12.1 us against 12.4 with four), else four (24 rows, 14336 x
+  // 4096 with 1 x 2 blocks: 20.1 against 22.5).
   if (pl.nt) {
-    pl.waves = pl.nt == 1 && kp >= 32 * kQ8Block ? 8 : 4;
+    pl.waves = pl.nt * pl.nn == 1 && kp >= 32 * kQ8Block ? 8 : 4;
     pl.split = TileSplit{};
   }
   return pl;
@@ -536,9 +528,9 @@ hipError_t launch_stream(const Q8Product &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int NT, int WAVES>
+template <int NT>
 hipError_t launch_stream(const Q8Product &p, int nn, hipStream_t st) {
-  return nn == 2 ? launch_stream<NT, 2, WAVES>(p, st) : launch_stream<NT, 1, WAVES>(p, st);
+  return nn == 2 ? launch_stream<NT, 2, 4>(p, st) : launch_stream<NT, 1, 4>(p, st);
 }
 
 }  // namespace
@@ -549,9 +541,10 @@ size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_d
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
   const Plan pl = plan_of(p.rows, p.outs, p.kp, p.out_dt);
-  if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, pl.nn, st) : launch_stream<1, 4>(p, pl.nn, st);
-  if (pl.nt == 2) return launch_stream<2, 4>(p, pl.nn, st);
-  if (pl.nt == 4) return launch_stream<4, 4>(p, pl.nn, st);
+  if (pl.waves == 8) return launch_stream<1, 1, 8>(p, st);
+  if (pl.nt == 1) return launch_stream<1>(p, pl.nn, st);
+  if (pl.nt == 2) return launch_stream<2>(p, pl.nn, st);
+  if (pl.nt == 4) return launch_stream<4>(p, pl.nn, st);
   const hipError_t e = pl.split.ta == 256   ? launch_tiles<256, 256>(p, pl.split, st)
                        : pl.split.tb == 256 ? launch_tiles<128, 256>(p, pl.split, st)
                                             : launch_tiles<128, 128>(p, pl.split, st);
