@@ -182,6 +182,22 @@ def test_product(t, n, k, transpose, dtype):
     check_sum(out, want, mag, n if transpose else k, (t, n, k, transpose), CUT if dtype == BF16 else 0.0)
 
 
+# (every shape of the streaming kernel's work-groups, its ring turning several times)
+@pytest.mark.parametrize("t,n,k", [(16, 1000, 3900), (7, 300, 8200), (1, 5001, 4301), (19, 2187, 1701), (21, 5001, 4301),
+                                   (39, 2767, 4301), (45, 4239, 4301)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_product_of_few_rows(t, n, k, transpose, dtype):
+    print(f"few rows {t} {n} {k} {transpose} {dtype}", flush=True)
+    rng = np.random.default_rng(t * 19 + n + k * 29)
+    a, av = rows_of(rng, t, k)
+    w, wv = weight_of(rng, k, n) if transpose else weight_of(rng, n, k)
+    wv = wv[:, :n] if transpose else wv.T
+    got = nsd.q8_matmul(a, w, transpose=transpose, dtype=dtype)
+    torch.cuda.synchronize()
+    check_sum(got, av @ wv, np.abs(av) @ np.abs(wv), k, (t, n, k), CUT if dtype == BF16 else 0.0)
+
+
 @pytest.mark.parametrize("t,n,k", PRODUCT_SIZES)
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_product_of_small_integers(t, n, k, dtype):
