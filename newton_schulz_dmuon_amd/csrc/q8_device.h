@@ -112,6 +112,37 @@ __device__ __forceinline__ TileOut tile_out(const TileWork &w, int ta, int tb, c
   return TileOut{base, out, dt, r * cols + c, cols, rows - r, cols - c};
 }
 
+// R runs of N (4 or 8) consecutive elements of base, `step` apart, all loads
+// before the first use.
+template <int N, int R>
+__device__ __forceinline__ void load_runs(const void *base, int32_t dt, int64_t at, int step, float (&v)[R][N]) {
+  if (dt == kF32) {
+    f32x4 w[R][N / 4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < N / 4; ++h) w[r][h] = *(const g_f32x4_at4 *)(static_cast<const float *>(base) + at + r * step + 4 * h);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[r][k] = w[r][k / 4][k % 4];
+  } else {
+    u32x2 w[R][N / 4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < N / 4; ++h)
+        w[r][h] = *(const g_u32x2_at2 *)(static_cast<const uint16_t *>(base) + at + r * step + 4 * h);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        v[r][2 * k] = __uint_as_float(w[r][k / 2][k % 2] << 16);
+        v[r][2 * k + 1] = __uint_as_float(w[r][k / 2][k % 2] & 0xffff0000u);
+      }
+  }
+}
+
 // N (4 or 8) consecutive outputs, plus base where there is one; `left` of them
 // exist.  Vector accesses at any element's address (8192 rows x 4095 bf16 outputs
 // of 512 codes each: 34 us, element by element 83); base may be out.
