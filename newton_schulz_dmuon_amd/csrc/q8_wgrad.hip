@@ -171,8 +171,8 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   auto load_x = [&](int step) {
     const int64_t t0 = static_cast<int64_t>(step) * kStep;
     const uint8_t *const xs = p.x + t0 * p.kp + k0, *const ss = p.sx + k0 / kQ8Block * t4 + t0;
-    // Rows behind the last are loaded as copies of it.  Their product is with
-    // zero rows of dy; a code NaN among them is in its columns' sums anyway.
+    // Rows behind the last are loaded as copies of it, with scales of other
+    // rows or the table's padding, and zeroed by zero_x_tail.
     const int last_row = rows_left(step) - 1, last_word = static_cast<int>(min(t4 - 4 - t0, static_cast<int64_t>(kStep)));
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -224,6 +224,28 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
     }
   };
 
+  // Zeroes the rows behind the last in stage `slot`, in the two groups that this
+  // wave wrote there for every column: a code under another row's scale may
+  // exceed bf16's range, and an infinity times dy's zero rows would be NaN.
+  const int full_steps = static_cast<int>(p.rows / kStep);
+  auto zero_x_tail = [&](int slot, int step) {
+    if (step < full_steps) return;
+    // opaque: no address is kept live across the loop for this
+    int l = lane_index();
+    asm volatile("" : "+v"(l));
+    for (int g = 2 * wn; g < 2 * wn + 2; ++g) {
+      const int first = max(rows_left(step) - 8 * g, 0);
+      if (first >= 8) continue;
+      for (int c = l; c < TK; c += 64) {
+        lds_char *const chunk = lds + slot * kXBytes + c * 128 + ((g ^ ((c & 15) >> 1) ^ (c & 1)) & 7) * 16;
+        if (first == 0)
+          *(lds_u32x4 *)chunk = u32x4{0, 0, 0, 0};
+        else
+          for (int r = first; r < 8; ++r) *(lds_u16 *)(chunk + 2 * r) = 0;
+      }
+    }
+  };
+
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -256,6 +278,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   if constexpr (H == 0) {
     load_x(tbeg);
     write_x(tbeg & 1);
+    zero_x_tail(tbeg & 1, tbeg);
     load_x(min(tbeg + 1, last));
   } else {
     issue_dy(s0, tbeg);
@@ -328,10 +351,12 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (H == 0)
+    if constexpr (H == 0) {
+      zero_x_tail((t + 1) & 1, min(t + 1, last));
       lds_barrier();
-    else
+    } else {
       barrier();
+    }
     __builtin_amdgcn_sched_barrier(0);
     const int s = s0;
     s0 = s1;
