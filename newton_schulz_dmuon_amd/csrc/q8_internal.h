@@ -11,9 +11,10 @@ namespace dmuon {
 
 // Elements that share one scale: along a row, and per side of a weight block.
 constexpr int kQ8Block = 128;
-// Range of the scale's exponent.  448 * 2^120 exceeds every finite fp32.  At
-// 2^-117 the smallest code, 2^-9, stands for 2^-126: every value that a code
-// and a scale stand for is a normal bf16 number.
+// Range of the scale's exponent.  448 * 2^120 exceeds every finite fp32, and so
+// do codes of 256 and more at 2^120, which the lowest values of bf16 and fp32
+// round to: expansions to bf16 use half the scale.  At 2^-117 the smallest code,
+// 2^-9, stands for 2^-126, fp32's and bf16's smallest normal number.
 constexpr int kQ8MinExp = -117, kQ8MaxExp = 120;
 // Rows of a scale table are a multiple of this many bytes.
 constexpr int kQ8ScaleRow = 4;

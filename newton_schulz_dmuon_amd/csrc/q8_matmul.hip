@@ -17,9 +17,12 @@
 // operands and 4e-5 with outlier channels, a hundredth of bf16's own rounding
 // (1.7e-3 of the norm), which is why a bf16 result takes it.
 //
-// fp32: the codes are expanded to bf16, code times scale, which is exact
-// (four significant bits), and multiplied by v_mfma_f32_16x16x32_bf16: every
-// product and sum is fp32's, at half the matrix rate.
+// fp32: the codes are expanded to bf16, code times half the scale, which is
+// exact (four significant bits; 448 * 2^119 is in range, 256 * 2^120, the code
+// of the lowest bf16 or fp32 value, would not be, and 2^-9 * 2^-118 is a
+// subnormal that expansion and product keep), and multiplied by
+// v_mfma_f32_16x16x32_bf16: every product and sum is fp32's, at half the matrix
+// rate.  The sums are a quarter of the result's and are multiplied by four.
 //
 // Weights b are the instruction's first operand and rows a the second: a lane
 // then holds four consecutive outputs of one row.
@@ -34,10 +37,13 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// 2^(byte - 127) as fp32, for a scale byte of the format.
-__device__ __forceinline__ float scale_of(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
+// 2^(byte - 128) as fp32, half of a scale byte's scale: what the expansion
+// multiplies by.
+__device__ __forceinline__ float half_scale(int byte) { return __uint_as_float(static_cast<uint32_t>(byte - 1) << 23); }
+// What the sums of expanded operands are multiplied by.
+template <bool EXACT> constexpr float kSumScale = EXACT ? 4.f : 1.f;
 
-// Eight codes (two dwords) times a scale as bf16, exactly.
+// Eight codes (two dwords) times a power of two as bf16, exactly.
 __device__ __forceinline__ bf16x8 expand8(int lo, int hi, float s) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
@@ -51,7 +57,7 @@ __device__ __forceinline__ bf16x8 expand8(int lo, int hi, float s) {
 template <bool EXACT>
 __device__ __forceinline__ f32x4 block_product(const i32x8 &b, int sb, const i32x8 &a, int sa, f32x4 acc) {
   if constexpr (EXACT) {
-    const float fb = scale_of(sb), fa = scale_of(sa);
+    const float fb = half_scale(sb), fa = half_scale(sa);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(b[2 * s], b[2 * s + 1], fb),
@@ -218,6 +224,7 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
     for (int w = 1; w < WAVES; ++w) sum += *part(w, b);
     const int64_t t = t0 + r16 * NT + b % NT, n = n0 + b / NT * 16 + 4 * g4;
     if (t >= p.rows) continue;
+    sum *= kSumScale<EXACT>;
     float v[4] = {sum[0], sum[1], sum[2], sum[3]};
     finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
   }
@@ -377,10 +384,10 @@ __device__ __forceinline__ void q8_tile(lds_char *const lds, const Q8Product &p,
     } else {
       // two half-steps of 64 codes, each read and multiplied in a phase of
       // its own; the loads are waited for at the end of the second
-      const float sw = scale_of(wb);
+      const float sw = half_scale(wb);
       float sr[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) sr[j] = scale_of(static_cast<int>((wa >> (8 * j)) & 0xff));
+      for (int j = 0; j < FN; ++j) sr[j] = half_scale(static_cast<int>((wa >> (8 * j)) & 0xff));
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         u32x4 fb[FM], fa[FN];
@@ -439,7 +446,7 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
       const int c = wm * (TA / 2) + (v * 4 + g4) * FM;
       float run[FM];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
+      for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v] * kSumScale<EXACT>;
       finish_run<FM>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
   }

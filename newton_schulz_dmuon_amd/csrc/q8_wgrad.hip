@@ -3,10 +3,12 @@
 //   out[n][k] = base[n][k] + sum_t dy[t][n] 2^e[k / 128][t] x[t][k]
 //
 // The sum runs over t, along which the checkpoint's scales change, so they
-// cannot ride on an 8-bit matrix instruction.  Code times scale is exact in
-// bf16 (four significant bits, an exponent within bf16's normal range), so x
-// is expanded to bf16 on its way into LDS and multiplied with the bf16
-// gradient; sums are fp32.
+// cannot ride on an 8-bit matrix instruction.  Code times half the scale is
+// exact in bf16 (four significant bits; 448 * 2^119 is in range, 256 * 2^120, the
+// code of the lowest bf16 or fp32 value, would not be, and 2^-9 * 2^-118 is a
+// subnormal that expansion and product keep), so x is expanded to bf16 on its way
+// into LDS and multiplied with the bf16 gradient; sums are fp32, half of the
+// result's.
 //
 // Bound by LDS reads and the matrix cores in turn: 8192 rows, 14336 x 4096
 // outputs, take 766 to 815 us, 1.2 PFLOP/s (a library bf16 product of that size
@@ -192,12 +194,15 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   // expands and transposes the loaded codes into stage `slot`
   auto write_x = [&](int slot) {
     const uint32_t at = x_at + static_cast<uint32_t>(slot * kXBytes);
+    // half the scales (the bytes are 10 or more, but for those behind the last
+    // row, which are the word's last)
+    const uint32_t half[2] = {sword[0] - 0x01010101u, sword[1] - 0x01010101u};
 #pragma unroll
     for (int c = 0; c < kWords; ++c) {
       uint32_t lo[8], hi[8];  // columns 4 c, 4 c + 1 and 4 c + 2, 4 c + 3 of row j
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float s = __uint_as_float(((sword[j >> 2] >> (8 * (j & 3))) & 0xff) << 23);
+        const float s = __uint_as_float(((half[j >> 2] >> (8 * (j & 3))) & 0xff) << 23);
         const int q = static_cast<int>(codes[j][c]);
         lo[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, false));
         hi[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, true));
@@ -381,6 +386,10 @@ void q8_wgrad_kernel(Q8WeightGrad p, TileSplit sp) {
     q8_wgrad_tile<TK, TN, 0>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
   else
     q8_wgrad_tile<TK, TN, 1>((lds_char *)smem, p, k0, n0, w.begin, w.end, acc);
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] *= 2.f;
 
   const int lane = lane_index(), r16 = lane & 15, g4 = lane >> 4;
   const int wm = static_cast<int>(wave >> 2), wn = static_cast<int>(wave & 3);
