@@ -26,6 +26,8 @@ ERR_HIP = -6
 
 BF16 = 0
 F32 = 1
+# with BF16, as dmuon_q8_matmul's out_dtype
+Q8_FAST_SUMS = 1 << 8
 FIELD_PARAM = 0
 FIELD_GRAD = 1
 FLAG_NS_FP32 = 1 << 0

@@ -59,6 +59,19 @@ int add_workspace(Buffers &b, void *workspace, size_t have, size_t need) {
   return b.add(workspace, static_cast<int64_t>(need), true, "workspace", 256);
 }
 
+// A product's out_dtype: the result's type, and whether its sums are fast.
+struct ProductType {
+  int32_t dt;
+  bool fast;
+};
+int product_type(int32_t out_dtype, ProductType &t) {
+  t.dt = out_dtype & ~static_cast<int32_t>(DMUON_Q8_FAST_SUMS);
+  t.fast = (out_dtype & DMUON_Q8_FAST_SUMS) != 0;
+  if (!dtype_ok(t.dt)) return fail(DMUON_ERR_UNSUPPORTED_DTYPE, "dtype code %d", out_dtype);
+  if (t.fast && t.dt != DMUON_BF16) return fail(DMUON_ERR_UNSUPPORTED_DTYPE, "fast sums take a bf16 result");
+  return DMUON_OK;
+}
+
 // No exception leaves a C entry.
 template <typename F>
 int guarded(F f) {
@@ -159,10 +172,10 @@ int dmuon_q8_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner, i
                                     size_t *out_bytes) {
   return guarded([&]() -> int {
     if (!out_bytes) return fail(DMUON_ERR_INVALID_ARG, "out_bytes is NULL");
-    if (!dtype_ok(out_dtype)) return fail(DMUON_ERR_UNSUPPORTED_DTYPE, "dtype code %d", out_dtype);
-    const int rc = check_sizes(rows, outs, inner);
-    if (rc) return rc;
-    *out_bytes = q8_matmul_workspace(rows, outs, round_up(inner, kQ8Block), out_dtype);
+    ProductType type;
+    int rc = product_type(out_dtype, type);
+    if (rc || (rc = check_sizes(rows, outs, inner))) return rc;
+    *out_bytes = q8_matmul_workspace(rows, outs, round_up(inner, kQ8Block), type.fast);
     return DMUON_OK;
   });
 }
@@ -171,9 +184,9 @@ int dmuon_q8_matmul(const void *codes, const void *scales, int64_t rows, const v
                     int64_t outs, int64_t inner, void *out, int32_t out_dtype, void *workspace,
                     size_t workspace_bytes, void *stream) {
   return guarded([&]() -> int {
-    if (!dtype_ok(out_dtype)) return fail(DMUON_ERR_UNSUPPORTED_DTYPE, "dtype code %d", out_dtype);
-    int rc = check_sizes(rows, outs, inner);
-    if (rc) return rc;
+    ProductType type;
+    int rc = product_type(out_dtype, type);
+    if (rc || (rc = check_sizes(rows, outs, inner))) return rc;
     if (rows == 0) return DMUON_OK;
     const int64_t kp = round_up(inner, kQ8Block), t4 = round_up(rows, kQ8ScaleRow), nkb = kp / kQ8Block;
     Buffers b;
@@ -181,8 +194,8 @@ int dmuon_q8_matmul(const void *codes, const void *scales, int64_t rows, const v
     if ((rc = b.add(scales, nkb * t4, false, "scales", 4))) return rc;
     if ((rc = b.add(codes_b, outs * kp, false, "codes_b"))) return rc;
     if ((rc = b.add(scales_b, round_up(outs, kQ8Block) / kQ8Block * nkb, false, "scales_b", 4))) return rc;
-    if ((rc = b.add(out, rows * outs * elem_size(out_dtype), true, "out"))) return rc;
-    if ((rc = add_workspace(b, workspace, workspace_bytes, q8_matmul_workspace(rows, outs, kp, out_dtype)))) return rc;
+    if ((rc = b.add(out, rows * outs * elem_size(type.dt), true, "out"))) return rc;
+    if ((rc = add_workspace(b, workspace, workspace_bytes, q8_matmul_workspace(rows, outs, kp, type.fast)))) return rc;
     if ((rc = b.check())) return rc;
     Q8Product p;
     p.a = static_cast<const uint8_t *>(codes);
@@ -194,7 +207,8 @@ int dmuon_q8_matmul(const void *codes, const void *scales, int64_t rows, const v
     p.rows = rows;
     p.outs = outs;
     p.kp = kp;
-    p.out_dt = out_dtype;
+    p.out_dt = type.dt;
+    p.fast = type.fast;
     return check_launch(launch_q8_matmul(p, static_cast<hipStream_t>(stream)), "q8 product launch");
   });
 }

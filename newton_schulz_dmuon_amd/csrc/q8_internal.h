@@ -74,8 +74,9 @@ struct Q8Product {
   float *ws;              // q8_matmul_workspace bytes
   int64_t rows, outs, kp;
   int32_t out_dt;
+  bool fast;              // the 8-bit instruction's sums in place of fp32's
 };
-size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt);
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, bool fast);
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st);
 
 // out[n][k] = base[n][k] + sum over t of dy[t][n] 2^(sx[k / 128][t] - 127) x[t][k]

@@ -2,27 +2,29 @@
 //
 //   out[t][n] = sum_b 2^(ea[b][t] + eb[n / 128][b]) sum_{k in block b} a[t][k] b[n][k]
 //
-// Two instructions do it, by the result's type.
+// Two instructions do it, by what the caller asks for.
 //
-// bf16: v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by 128 x 16
-// codes and applies each operand's power-of-two scale inside the instruction,
-// so the block scales cost no arithmetic and one fp32 accumulator runs through
-// all of K.  It takes 128 elements of k, one block of the format: both
-// operands' scales are constant over it, and any order of k inside it will do
-// as long as both operands use the same.  The instruction (like every 8-bit
-// one here, of either depth) adds the products of eight consecutive codes of a
-// lane with 14 bits: aligned to the largest exponent of the eight, 2^E, each
-// product is cut toward zero at 2^(E - 13); the groups of eight then add in
-// fp32.  Against exact sums that is 1.5e-5 of the result's norm on Gaussian
-// operands and 4e-5 with outlier channels, a hundredth of bf16's own rounding
-// (1.7e-3 of the norm), which is why a bf16 result takes it.
-//
-// fp32: the codes are expanded to bf16, code times half the scale, which is
-// exact (four significant bits; 448 * 2^119 is in range, 256 * 2^120, the code
-// of the lowest bf16 or fp32 value, would not be, and 2^-9 * 2^-118 is a
+// fp32 sums (EXACT): the codes are expanded to bf16, code times half the scale,
+// which is exact (four significant bits; 448 * 2^119 is in range, 256 * 2^120,
+// the code of the lowest bf16 or fp32 value, would not be, and 2^-9 * 2^-118 is a
 // subnormal that expansion and product keep), and multiplied by
-// v_mfma_f32_16x16x32_bf16: every product and sum is fp32's, at half the matrix
-// rate.  The sums are a quarter of the result's and are multiplied by four.
+// v_mfma_f32_16x16x32_bf16: every product and sum is fp32's, at half the 8-bit
+// matrix rate.  The sums are a quarter of the result's and are multiplied by
+// four.
+//
+// Fast sums, for a bf16 result: v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16
+// x 128 by 128 x 16 codes and applies each operand's power-of-two scale inside
+// the instruction, so the block scales cost no arithmetic and one fp32
+// accumulator runs through all of K.  It takes 128 elements of k, one block of
+// the format: both operands' scales are constant over it, and any order of k
+// inside it will do as long as both operands use the same.  The instruction
+// (like every 8-bit one here, of either depth) adds the products of eight
+// consecutive codes of a lane with 14 bits: aligned to the largest exponent of
+// the eight, 2^E, each product is cut toward zero at 2^(E - 13); the groups of
+// eight then add in fp32.  Against exact sums that is 1.5e-5 of the result's
+// norm on Gaussian operands and 4e-5 with outlier channels (bf16's own rounding:
+// 1.7e-3), but where large products cancel nothing of the small ones may be
+// left.  Hence it is the caller's choice.
 //
 // Weights b are the instruction's first operand and rows a the second: a lane
 // then holds four consecutive outputs of one row.
@@ -249,11 +251,12 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 // neighbours' follow, and block j, column r of the rows' operand holds row
 // r * FN + j, so that a lane's FN scale bytes are one LDS word.
 //
-// Bound by the matrix cores at the clock they leave: 8192 rows of a 14336 x
-// 4096 weight take 351 to 381 us, 2.53 to 2.74 PFLOP/s (a library 8-bit product
-// with one scale 2.5).  fp32 results, which multiply in bf16 and expand in the
-// same phase, 2001 rows by a transposed 18944 x 3584 weight: 210 to 218 us, 1.3
-// PFLOP/s (a library bf16 product 1.38).
+// Bound by the matrix cores at the clock they leave: with fp32 sums, which
+// multiply in bf16 and expand in the same phase, 8192 rows of a 14336 x 4096
+// weight take 646 to 659 us, 1.46 to 1.49 PFLOP/s, and 2001 rows by a transposed
+// 18944 x 3584 weight 210 to 218, 1.3 (a library bf16 product 1.38).  With fast
+// sums the first takes 351 to 381 us, 2.53 to 2.74 PFLOP/s (a library 8-bit
+// product with one scale 2.5).
 constexpr int kTileThreads = 512;
 constexpr int kRowBytes = 128;
 
@@ -456,13 +459,13 @@ void q8_tile_kernel(Q8Product p, TileSplit sp) {
 
 namespace {
 
-// Microseconds a step of one K block, measured on 80 .. 8192 rows.  bf16: 256 x
-// 256 tiles 1.03 with one work-group on the chip and 1.5 with 256 (the clock
+// Microseconds a step of one K block, measured on 80 .. 8192 rows.  Fast sums: 256
+// x 256 tiles 1.03 with one work-group on the chip and 1.5 with 256 (the clock
 // gives way), 128 x 256 tiles 0.8 and 0.97, 128 x 128 tiles 0.6 alone on their
 // CU and 1.06 for two.  The best with each: 2048 rows of a 4096 x 8192 weight 73
 // us, 65.5 and 71; 1024 rows of a 4096 x 4096 one 38, 31 and 26; 4096 rows 56, 73
-// and 76.  fp32 results of the first: 117, 112 and 127.
-constexpr std::initializer_list<TileCost> kBf16Costs = {
+// and 76.  fp32 sums of the first: 117, 112 and 127.
+constexpr std::initializer_list<TileCost> kFastCosts = {
     {256, 256, 1, 1.03f, 1.5f}, {128, 256, 1, 0.8f, 0.97f}, {128, 128, 2, 0.6f, 1.06f}};
 constexpr std::initializer_list<TileCost> kExactCosts = {
     {256, 256, 1, 2.23f, 2.9f}, {128, 256, 1, 1.38f, 1.68f}, {128, 128, 2, 0.95f, 1.88f}};
@@ -479,7 +482,11 @@ struct Plan {
 // codes at 53 GB/s, 256 of them at a time, while the weight comes from memory at
 // 4.9 TB/s; a quarter of the shorter of the two does not hide.  64 rows of a
 // 14336 x 4096 weight: 21 us with 4 x 2 blocks a work-group, 39 with one, 25 in
-// tiles; of a 4096 x 14336 one: 20.5 with 2 x 2, 36 and 24.
+// tiles; of a 4096 x 14336 one: 20.5 with 2 x 2, 36 and 24.  Those are fast sums;
+// fp32 sums take 21.7, 40 and 28.4, and 20.9, 36 and 27: bound alike, so one
+// model serves both (over 12 shapes its choice is the best for fp32 sums in ten
+// and within 12%; 256 rows of a 4096 x 4096 weight 16.3 us, fast 13.6, in tiles
+// 21.7 and 18.6).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
   const float bytes = static_cast<float>((16 * nn + std::min<int64_t>(16 * nt, rows)) * kp);
@@ -488,14 +495,15 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
 }
 // Rows up to which it is considered: 512 rows of a 256 x 1536 weight take 3.2 us
-// against 10.0 in tiles, of a 1024 x 4096 one 7.9 against 16.6.
+// against 10.0 in tiles (fp32 sums 3.5 and 11), of a 1024 x 4096 one 7.9 against
+// 16.6 (9.0 and 19.8).
 constexpr int64_t kStreamRows = 1024;
 
-Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
+Plan plan_of(int64_t rows, int64_t outs, int64_t kp, bool fast) {
   Plan pl{};
   if (rows == 0) return pl;
   float us;
-  pl.split = choose_split(outs, rows, kp / kQ8Block, out_dt == kF32 ? kExactCosts : kBf16Costs, &us);
+  pl.split = choose_split(outs, rows, kp / kQ8Block, fast ? kFastCosts : kExactCosts, &us);
   if (rows > kStreamRows) return pl;
   for (const int nt : {1, 2, 4})
     for (const int nn : {1, 2}) {
@@ -518,7 +526,7 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
 template <int TA, int TB>
 hipError_t launch_tiles(const Q8Product &p, const TileSplit &sp, hipStream_t st) {
   const dim3 grid(sp.whole + sp.tail * sp.pieces);
-  if (p.out_dt == kF32)
+  if (!p.fast)
     hipLaunchKernelGGL((q8_tile_kernel<TA, TB, true>), grid, dim3(kTileThreads), 0, st, p, sp);
   else
     hipLaunchKernelGGL((q8_tile_kernel<TA, TB, false>), grid, dim3(kTileThreads), 0, st, p, sp);
@@ -528,7 +536,7 @@ hipError_t launch_tiles(const Q8Product &p, const TileSplit &sp, hipStream_t st)
 template <int NT, int NN, int WAVES>
 hipError_t launch_stream(const Q8Product &p, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN) * ((p.rows + 16 * NT - 1) / (16 * NT))));
-  if (p.out_dt == kF32)
+  if (!p.fast)
     hipLaunchKernelGGL((q8_stream_kernel<NT, NN, WAVES, true>), grid, dim3(WAVES * 64), 0, st, p);
   else
     hipLaunchKernelGGL((q8_stream_kernel<NT, NN, WAVES, false>), grid, dim3(WAVES * 64), 0, st, p);
@@ -542,12 +550,12 @@ hipError_t launch_stream(const Q8Product &p, int nn, hipStream_t st) {
 
 }  // namespace
 
-size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, int32_t out_dt) {
-  return plan_of(rows, outs, kp, out_dt).split.ws_bytes();
+size_t q8_matmul_workspace(int64_t rows, int64_t outs, int64_t kp, bool fast) {
+  return plan_of(rows, outs, kp, fast).split.ws_bytes();
 }
 
 hipError_t launch_q8_matmul(const Q8Product &p, hipStream_t st) {
-  const Plan pl = plan_of(p.rows, p.outs, p.kp, p.out_dt);
+  const Plan pl = plan_of(p.rows, p.outs, p.kp, p.fast);
   if (pl.waves == 8) return launch_stream<1, 1, 8>(p, st);
   if (pl.nt == 1) return launch_stream<1>(p, pl.nn, st);
   if (pl.nt == 2) return launch_stream<2>(p, pl.nn, st);

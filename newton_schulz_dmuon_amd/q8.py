@@ -234,10 +234,16 @@ def _workspace(call, sizes, workspace: Optional[Workspace], device, stream):
 
 
 def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=None,
-              workspace: Optional[Workspace] = None, stream=None):
+              workspace: Optional[Workspace] = None, stream=None, fast_sums: bool = False):
     """``a w^T`` (``[rows, w.rows]``) or, with ``transpose``, ``a w``
-    (``[rows, w.cols]``), bf16 (the default) or fp32: fp32 sums, one rounding.
-    ``out`` takes the result; its dtype is then the result's."""
+    (``[rows, w.cols]``), bf16 (the default) or fp32: exact products, fp32 sums,
+    one rounding.  ``out`` takes the result; its dtype is then the result's.
+
+    With ``fast_sums``, for a bf16 result, the sums are the 8-bit matrix
+    instruction's, twice as fast for many rows: products are added in groups of
+    eight, each cut toward zero at 2^-13 of the group's largest.  That adds an
+    error of 1.5e-5 of the result's norm on Gaussian operands, 4e-5 with outlier
+    channels, and at most 7 * 2^-13 of the products' sum of magnitudes."""
     import torch
     rows, device = a.codes.shape[0], a.codes.device
     codes, scales = (w.codes_t, w.scales_t) if transpose else (w.codes, w.scales)
@@ -262,6 +268,8 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
         _check_tensor(out, "out", (rows, outs), out.dtype, device)
     lib = load()
     dt = _dtype_code(out)
+    if fast_sums:
+        dt |= _lib.Q8_FAST_SUMS
     ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner, dt),
                                workspace, device, stream)
     _run(lib.dmuon_q8_matmul, device, stream, a.codes.data_ptr(), a.scales.data_ptr(), rows,
