@@ -7,6 +7,7 @@ here only fills the C structs and checks the returned status.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -42,16 +43,30 @@ def _stream_handle(device, stream) -> Optional[int]:
     return stream.cuda_stream
 
 
-def _keep_for_stream(t, device, stream) -> None:
-    """PyTorch's caching allocator ties a block to the stream that allocated
-    it and may hand it out again as soon as the tensor is freed.  A buffer
-    allocated on the current stream but used by kernels on another one is
-    marked as in use by that stream too, so that neither its release (a
-    temporary workspace) nor its replacement (a growing Workspace) lets a
-    new tensor take the memory before those kernels are done."""
+def _raw_stream(index: int) -> int:
+    """The handle of a device's current stream.  PyTorch has it without a
+    Stream object around it, a microsecond and a half cheaper."""
     import torch
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        t.record_stream(stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _allocating(stream):
+    """A context whose allocations belong to ``stream`` (None: the current one).
+    PyTorch's caching allocator hands a freed block out again at once to the
+    stream that it belongs to, whose work is in order.  Kernels on another stream
+    would write such a block while earlier work of its own may still use it."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _mark_used(stream, *tensors) -> None:
+    """Marks tensors as used by ``stream``, so that their memory goes to no other
+    tensor before its work that is enqueued when they are freed is done (nothing
+    is to be marked for the stream that they belong to)."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 @dataclass
@@ -165,17 +180,29 @@ def workspace_bytes(params, opts: StepOptions) -> int:
 
 
 class Workspace:
-    """Device scratch for ``muon_step``, grown on demand (PyTorch allocates)."""
+    """Device scratch for ``muon_step`` and the 8-bit products, grown on demand
+    (PyTorch allocates)."""
 
     def __init__(self):
         self.buf = None
+        self._owner = None  # the handle of the stream that buf belongs to
 
-    def get(self, nbytes: int, device):
+    def get(self, nbytes: int, device, stream=None):
+        """At least ``nbytes`` on ``device``, for a call on ``stream`` (None:
+        the device's current one)."""
         import torch
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
             self.buf = None
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            with _allocating(stream):
+                self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self._owner = self._handle(device, stream)
+        elif self._handle(device, stream) != self._owner:
+            _mark_used(stream if stream is not None else torch.cuda.current_stream(device), self.buf)
         return self.buf
+
+    @staticmethod
+    def _handle(device, stream) -> int:
+        return stream.cuda_stream if stream is not None else _raw_stream(device.index)
 
 
 def muon_step(params: Sequence, grads: Sequence, momenta: Sequence, scales: Sequence[float],
@@ -199,8 +226,7 @@ def muon_step(params: Sequence, grads: Sequence, momenta: Sequence, scales: Sequ
     lib = load()
     need = ctypes.c_size_t(0)
     check(lib.dmuon_workspace_bytes(arr, n, ctypes.byref(cfg), ctypes.byref(need)))
-    ws = (workspace or Workspace()).get(need.value, device)
-    _keep_for_stream(ws, device, stream)
+    ws = (workspace or Workspace()).get(need.value, device, stream)
     if packed is None:
         check(lib.dmuon_muon_step(arr, n, ctypes.byref(cfg), ws.data_ptr(), ws.numel(),
                                   _stream_handle(device, stream)))

@@ -19,7 +19,10 @@ A training step of one linear layer::
 The functions enqueue kernels on ``stream`` (the current one by default) and
 record no gradients: the backward pass is the last two calls.  Results that are
 not passed in are new tensors; without ``workspace`` a call that needs scratch
-allocates it.  A ``Workspace`` serves any number of calls on one stream; work
+allocates it.  On a ``stream`` of its own a call's results and scratch belong to
+that stream, and all its tensors may be dropped as soon as it returns; the caller
+only orders the streams (``stream`` after the work that makes the inputs, the
+readers of the results after ``stream``).  A ``Workspace`` serves any number of calls on one stream; work
 that may overlap (calls on two streams, a call and a replayed graph, two graphs)
 needs one each.  Every call can be captured into a graph, and the same call
 gives the same bits.
@@ -32,7 +35,7 @@ from typing import List, Optional, Sequence
 
 from . import _lib
 from ._lib import DmuonError, Q8WeightDesc, check, load
-from .api import Workspace, _dtype_code, _keep_for_stream, _ptr
+from .api import Workspace, _allocating, _dtype_code, _mark_used, _ptr, _raw_stream
 
 BLOCK = 128
 
@@ -131,8 +134,6 @@ def _run(fn, device, stream, *args) -> None:
     if stream is None:
         handle = _raw_stream(index)
     else:
-        if stream.device != device:
-            raise _invalid(f"the stream is on {stream.device}, the tensors on {device}")
         handle = stream.cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)
@@ -143,35 +144,36 @@ def _run(fn, device, stream, *args) -> None:
         check(status)
 
 
-def _raw_stream(index: int) -> int:
-    """The handle of a device's current stream.  PyTorch has it without a
-    Stream object around it, a microsecond and a half cheaper."""
+def _check_stream(device, stream) -> None:
+    if stream is not None and stream.device != device:
+        raise _invalid(f"the stream is on {stream.device}, the tensors on {device}")
+
+
+def _keep(device, stream, made=(), given=()) -> None:
+    """For a call on a stream of its own: the memory of every tensor of it stays
+    theirs until the stream is done with it, and that of results made for the
+    call (which belongs to ``stream``) until the current stream is."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
-
-
-def _allocated(device, stream, *tensors) -> None:
-    """Outputs and workspaces made here on the current stream and used on
-    another one are marked as in use by that stream too."""
     if stream is not None:
-        for t in tensors:
-            if t is not None:
-                _keep_for_stream(t, device, stream)
+        _mark_used(torch.cuda.current_stream(device), *made)
+        _mark_used(stream, *given)
 
 
 def q8_quantize(x, out: Optional[Q8Rows] = None, stream=None) -> Q8Rows:
     """8-bit rows of ``x`` (bf16 or fp32, ``[..., cols]``; the leading
     dimensions are flattened), one scale per 1 x 128 block."""
     device, rows, cols = _matrix(x, "x")
+    _check_stream(device, stream)
     dt = _dtype_code(x)
     if out is None:
-        out = Q8Rows.empty(rows, cols, device)
-        _allocated(device, stream, out.codes, out.scales)
+        with _allocating(stream):
+            out = Q8Rows.empty(rows, cols, device)
+        _keep(device, stream, made=(out.codes, out.scales))
     else:
         if out.cols != cols or out.codes.device != device:
             raise _invalid("out does not fit x")
         _check_rows(out, rows)
+    _keep(device, stream, given=(x, out.codes, out.scales))
     _run(load().dmuon_q8_quantize, device, stream, _ptr(x), dt, rows, cols, out.codes.data_ptr(),
          out.scales.data_ptr())
     return out
@@ -193,10 +195,12 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
             raise _invalid(f"matrix {i} is not 2-D")
         if not p.is_cuda or p.device != device:
             raise _invalid(f"matrix {i} is on {p.device}, not on {device} (a GPU)")
+    _check_stream(device, stream)
     if out is None:
-        out = [Q8Weight.empty(p.shape[0], p.shape[1], device, transposed) for p in params]
+        with _allocating(stream):
+            out = [Q8Weight.empty(p.shape[0], p.shape[1], device, transposed) for p in params]
         for q in out:
-            _allocated(device, stream, q.codes, q.scales, q.codes_t, q.scales_t)
+            _keep(device, stream, made=(q.codes, q.scales, q.codes_t, q.scales_t))
     else:
         out = list(out)
         if len(out) != n:
@@ -217,6 +221,7 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
         arr[i] = Q8WeightDesc(_ptr(p), _dtype_code(p), 0, p.shape[0], p.shape[1],
                               q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.codes_t),
                               _ptr(q.scales_t))
+        _keep(device, stream, given=(p, q.codes, q.scales, q.codes_t, q.scales_t))
     _run(load().dmuon_q8_quantize_weights, device, stream, arr, n)
     return out
 
@@ -228,8 +233,7 @@ def _workspace(call, sizes, workspace: Optional[Workspace], device, stream):
     check(call(*sizes, ctypes.byref(need)))
     if need.value == 0:
         return None, 0, None
-    buf = (workspace or Workspace()).get(need.value, device)
-    _keep_for_stream(buf, device, stream)
+    buf = (workspace or Workspace()).get(need.value, device, stream)
     return buf.data_ptr(), buf.numel(), buf
 
 
@@ -252,6 +256,7 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
     outs, inner = (w.cols, w.rows) if transpose else (w.rows, w.cols)
     if not a.codes.is_cuda:
         raise _invalid(f"codes are on {device}, not on a GPU")
+    _check_stream(device, stream)
     if a.cols != inner:
         raise _invalid(f"rows of {a.cols} columns against a weight of {inner}")
     _check_rows(a, rows)
@@ -260,8 +265,9 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
     _check_tensor(scales, "the weight's scales", (_up(outs, BLOCK) // BLOCK, kp // BLOCK),
                   torch.uint8, device)
     if out is None:
-        out = torch.empty(rows, outs, dtype=dtype or torch.bfloat16, device=device)
-        _allocated(device, stream, out)
+        with _allocating(stream):
+            out = torch.empty(rows, outs, dtype=dtype or torch.bfloat16, device=device)
+        _keep(device, stream, made=(out,))
     else:
         if dtype is not None and dtype != out.dtype:
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
@@ -272,6 +278,7 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
         dt |= _lib.Q8_FAST_SUMS
     ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner, dt),
                                workspace, device, stream)
+    _keep(device, stream, given=(a.codes, a.scales, codes, scales, out))
     _run(lib.dmuon_q8_matmul, device, stream, a.codes.data_ptr(), a.scales.data_ptr(), rows,
          codes.data_ptr(), scales.data_ptr(), outs, inner, out.data_ptr(), dt, ws, nws)
     return out
@@ -287,6 +294,7 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
     the gradient in place."""
     import torch
     device, rows, outs = _matrix(dy, "dy")
+    _check_stream(device, stream)
     if dy.dtype != torch.bfloat16:
         raise DmuonError(_lib.ERR_UNSUPPORTED_DTYPE, f"dy has dtype {dy.dtype}, not torch.bfloat16")
     if not dy.is_contiguous():
@@ -296,9 +304,10 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
     _check_rows(x, rows)
     cols = x.cols
     if out is None:
-        out = torch.empty(outs, cols, device=device,
-                          dtype=dtype or (base.dtype if base is not None else torch.bfloat16))
-        _allocated(device, stream, out)
+        with _allocating(stream):
+            out = torch.empty(outs, cols, device=device,
+                              dtype=dtype or (base.dtype if base is not None else torch.bfloat16))
+        _keep(device, stream, made=(out,))
     else:
         if dtype is not None and dtype != out.dtype:
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
@@ -308,6 +317,7 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
     lib = load()
     ws, nws, keep = _workspace(lib.dmuon_q8_weight_grad_workspace_bytes, (rows, outs, cols),
                                workspace, device, stream)
+    _keep(device, stream, given=(dy, x.codes, x.scales, base, out))
     _run(lib.dmuon_q8_weight_grad, device, stream, dy.data_ptr(), x.codes.data_ptr(),
          x.scales.data_ptr(), rows, outs, cols, base.data_ptr() if base is not None else None,
          out.data_ptr(), _dtype_code(out), ws, nws)
