@@ -60,6 +60,15 @@ def _allocating(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _capturing(device, stream) -> bool:
+    """Whether ``stream`` (None: the device's current one) records a graph."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _mark_used(stream, *tensors) -> None:
     """Marks tensors as used by ``stream``, so that their memory goes to no other
     tensor before its work that is enqueued when they are freed is done (nothing
@@ -181,10 +190,13 @@ def workspace_bytes(params, opts: StepOptions) -> int:
 
 class Workspace:
     """Device scratch for ``muon_step`` and the 8-bit products, grown on demand
-    (PyTorch allocates)."""
+    (PyTorch allocates).  Buffers that were used in a graph's capture are kept
+    when a larger call replaces them, since the graph's replays write them; a
+    Workspace has to live as long as the graphs captured with it."""
 
     def __init__(self):
         self.buf = None
+        self._captured = []  # buffers that graphs use
         self._owner = None  # the handle of the stream that buf belongs to
 
     def get(self, nbytes: int, device, stream=None):
@@ -198,6 +210,8 @@ class Workspace:
             self._owner = self._handle(device, stream)
         elif self._handle(device, stream) != self._owner:
             _mark_used(stream if stream is not None else torch.cuda.current_stream(device), self.buf)
+        if _capturing(device, stream) and not any(b is self.buf for b in self._captured):
+            self._captured.append(self.buf)
         return self.buf
 
     @staticmethod

@@ -22,9 +22,10 @@ not passed in are new tensors; without ``workspace`` a call that needs scratch
 allocates it.  On a ``stream`` of its own a call's results and scratch belong to
 that stream, and all its tensors may be dropped as soon as it returns; the caller
 only orders the streams (``stream`` after the work that makes the inputs, the
-readers of the results after ``stream``).  A ``Workspace`` serves any number of calls on one stream; work
-that may overlap (calls on two streams, a call and a replayed graph, two graphs)
-needs one each.  Every call can be captured into a graph, and the same call
+readers of the results after ``stream``).  A ``Workspace`` serves
+any number of calls on one stream; work that may overlap (calls on two streams, a
+call and a replayed graph, two graphs) needs one each, and a graph's has to live
+as long as the graph.  Every call can be captured into a graph, and the same call
 gives the same bits.
 """
 

@@ -159,3 +159,32 @@ def test_inputs_may_be_dropped_after_a_call():
         torch.cuda.synchronize()
         assert torch.equal(y, want)
         del junk
+
+
+def test_a_captured_workspace_outlives_a_larger_call():
+    """Captured with a warmed Workspace, which a larger layer then uses eagerly:
+    the graph's scratch goes to no new tensor, and its replays stay right."""
+    print("captured workspace", flush=True)
+    small, large = layer_inputs(50, 2048, 384, 1536), layer_inputs(51, 8192, 1024, 2048)
+    ws = nsd.Workspace()
+
+    def grad(inputs, ws):
+        x, dy, _, base = inputs
+        return nsd.q8_weight_grad(dy, nsd.q8_quantize(x), base=base, workspace=ws)
+
+    want, want_large = grad(small, None), grad(large, None)
+    grad(small, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = grad(small, ws)
+    scratch, nbytes = ws.buf.data_ptr(), ws.buf.numel()
+    for _ in range(3):
+        assert torch.equal(grad(large, ws), want_large)
+        assert ws.buf.numel() > nbytes
+        torch.cuda.synchronize()
+        held = [torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(h.data_ptr() != scratch for h in held)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all((h == 7).all() for h in held)

@@ -2,6 +2,8 @@
 that record which of them is current when memory is allocated."""
 
 import contextlib
+import gc
+import weakref
 
 import pytest
 import torch
@@ -13,6 +15,7 @@ from newton_schulz_dmuon_amd import api  # noqa: E402
 class Stream:
     def __init__(self, handle):
         self.cuda_stream = handle
+        self.capturing = False
 
 
 class Buffer:
@@ -39,6 +42,8 @@ def streams(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", use)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
     monkeypatch.setattr(torch, "empty", lambda n, dtype, device: Buffer(current[-1], n))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[-1].capturing)
     monkeypatch.setattr(api, "_raw_stream", lambda index: current[-1].cuda_stream)
     return current
 
@@ -66,3 +71,23 @@ def test_other_streams_are_recorded(streams):
     assert ws.get(500, DEVICE, s) is buf and buf.users == [s]
     with torch.cuda.stream(s):
         assert ws.get(500, DEVICE) is buf and buf.users == [s, s]
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_a_captured_buffer_is_kept(streams, other):
+    """Warmed, captured, then grown by an eager call: the graph still writes the
+    first buffer."""
+    s = Stream(2) if other else None
+    ws = api.Workspace()
+    first = weakref.ref(ws.get(1000, DEVICE, s))
+    (s or streams[0]).capturing = True
+    ws.get(1000, DEVICE, s)
+    ws.get(800, DEVICE, s)
+    (s or streams[0]).capturing = False
+    second = weakref.ref(ws.get(2000, DEVICE, s))
+    assert ws.get(4000, DEVICE, s).numel() == 4000
+    gc.collect()
+    assert first() is not None and second() is None  # the second was in no capture
+    del ws
+    gc.collect()
+    assert first() is None
