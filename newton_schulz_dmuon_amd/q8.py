@@ -185,7 +185,8 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
     """8-bit weights of each matrix (bf16 or fp32, ``[rows, cols]``), one scale
     per 128 x 128 block; without ``transposed`` only what the forward product
     reads.  All matrices lie on one device.  ``out`` takes an earlier call's
-    results, with or without their transposed codes, and overwrites them."""
+    results, with or without their transposed codes, and overwrites them, their
+    ``rows`` and ``cols`` too (columns that round up to the same 128 fit)."""
     import torch
     n = len(params)
     if n == 0:
@@ -224,6 +225,8 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
                               _ptr(q.scales_t))
         _keep(device, stream, given=(p, q.codes, q.scales, q.codes_t, q.scales_t))
     _run(load().dmuon_q8_quantize_weights, device, stream, arr, n)
+    for p, q in zip(params, out):
+        q.rows, q.cols = p.shape
     return out
 
 
