@@ -17,7 +17,9 @@ A training step of one linear layer::
     nsd.muon_step([w], [grad], [momentum], [scale])
 
 The functions enqueue kernels on ``stream`` (the current one by default) and
-record no gradients: the backward pass is the last two calls.  Results that are
+record no gradients: the backward pass is the last two calls.  An input that
+requires one is refused while gradients are recorded (parameters that
+``q8_quantize_weights`` reads excepted).  Results that are
 not passed in are new tensors; without ``workspace`` a call that needs scratch
 allocates it.  On a ``stream`` of its own a call's results and scratch belong to
 that stream, and all its tensors may be dropped as soon as it returns; the caller
@@ -117,8 +119,18 @@ def _check_rows(q: Q8Rows, rows: int) -> None:
     _check_tensor(q.scales, "scales", (kp // BLOCK, _up(rows, 4)), torch.uint8, q.codes.device)
 
 
+def _check_untracked(t, what: str) -> None:
+    """No result carries a gradient on: an input that autograd tracks would leave
+    its graph without a word."""
+    import torch
+    if t.requires_grad and torch.is_grad_enabled():
+        raise _invalid(f"{what} requires a gradient, which this call does not record; call it under "
+                       "torch.no_grad(), in an autograd.Function or on a detached tensor")
+
+
 def _matrix(t, what: str):
     """``t``'s device, rows and columns; any leading dimensions are rows."""
+    _check_untracked(t, what)
     if t.dim() < 1 or t.shape[-1] < 1:
         raise _invalid(f"{what} needs at least one column")
     if not t.is_cuda:
@@ -191,6 +203,9 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
     n = len(params)
     if n == 0:
         return []
+    for i, p in enumerate(params):
+        if not p.is_leaf:  # a parameter may be quantised, as the step may update it
+            _check_untracked(p, f"matrix {i}")
     device = params[0].device
     for i, p in enumerate(params):
         if p.dim() != 2:
@@ -317,6 +332,7 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
         _check_tensor(out, "out", (outs, cols), out.dtype, device)
     if base is not None:
+        _check_untracked(base, "base")
         _check_tensor(base, "base", (outs, cols), out.dtype, device)
     lib = load()
     ws, nws, keep = _workspace(lib.dmuon_q8_weight_grad_workspace_bytes, (rows, outs, cols),
