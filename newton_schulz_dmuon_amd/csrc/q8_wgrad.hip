@@ -32,19 +32,8 @@ constexpr int kHalfBytes = kStep * 256;  // 128 bf16 columns of a step
 // transposing reads below (16 rows x 32 bytes) touch distinct banks.
 __device__ __forceinline__ int swz(int row) { return ((row & 3) | (((row >> 3) & 1) << 2)) << 1; }
 
-// Four consecutive t of one column: within 16 lanes, lane 4 e + q names row
-// t0 + e, columns 4 q .. 4 q + 3, and lane j receives rows t0 .. t0 + 3 of
-// column j.  Inline assembly, because before the builtin the compiler waits
-// for every LDS-bound load in flight (it cannot tell the stages apart).  The
-// result is not there until wait_fragments(), which names it, and nothing but
-// further reads may come between.
-__device__ __forceinline__ u32x2 read_transposed(uint32_t lds_addr) {
-  u32x2 r;
-  asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(r) : "v"(lds_addr));
-  return r;
-}
-
-// An MFMA operand: two such reads, eight consecutive t.
+// An MFMA operand: eight consecutive t of one column, by two transposing reads
+// of four.
 struct Fragment {
   u32x2 lo, hi;
   __device__ __forceinline__ bf16x8 get() const {
@@ -52,16 +41,43 @@ struct Fragment {
   }
 };
 
-// Waits for this wave's LDS reads, tied to two or four fragments so that
-// no use of them moves above it.
-__device__ __forceinline__ void wait_fragments(Fragment &a, Fragment &b) {
-  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(a.lo), "+v"(a.hi), "+v"(b.lo), "+v"(b.hi));
+// A step's fragments of FN 16-column blocks, from the blocks' addresses in dy's
+// stage.  A read gives four consecutive t of one column: within 16 lanes, lane 4
+// e + q names row t0 + e, columns 4 q .. 4 q + 3, and lane j receives rows t0 ..
+// t0 + 3 of column j; rows are 256 bytes apart.  Inline assembly, because before
+// the builtin the compiler waits for every LDS-bound load in flight (it cannot
+// tell the stages apart); one block with its wait, so that no register that a
+// read is still to fill is seen outside it.  The wait covers the LDS reads before
+// it, too.
+__device__ __forceinline__ void read_fragments(const uint32_t (&at)[4], Fragment (&f)[2][4]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %2, %17\n\tds_read_b64_tr_b16 %3, %17 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %4, %18\n\tds_read_b64_tr_b16 %5, %18 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %6, %19\n\tds_read_b64_tr_b16 %7, %19 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %8, %16 offset:8192\n\tds_read_b64_tr_b16 %9, %16 offset:9216\n\t"
+      "ds_read_b64_tr_b16 %10, %17 offset:8192\n\tds_read_b64_tr_b16 %11, %17 offset:9216\n\t"
+      "ds_read_b64_tr_b16 %12, %18 offset:8192\n\tds_read_b64_tr_b16 %13, %18 offset:9216\n\t"
+      "ds_read_b64_tr_b16 %14, %19 offset:8192\n\tds_read_b64_tr_b16 %15, %19 offset:9216\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0][0].lo), "=&v"(f[0][0].hi), "=&v"(f[0][1].lo), "=&v"(f[0][1].hi), "=&v"(f[0][2].lo),
+        "=&v"(f[0][2].hi), "=&v"(f[0][3].lo), "=&v"(f[0][3].hi), "=&v"(f[1][0].lo), "=&v"(f[1][0].hi),
+        "=&v"(f[1][1].lo), "=&v"(f[1][1].hi), "=&v"(f[1][2].lo), "=&v"(f[1][2].hi), "=&v"(f[1][3].lo),
+        "=&v"(f[1][3].hi)
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+      : "memory");
 }
-__device__ __forceinline__ void wait_fragments(Fragment (&f)[2]) { wait_fragments(f[0], f[1]); }
-__device__ __forceinline__ void wait_fragments(Fragment (&f)[4]) {
-  asm volatile("s_waitcnt lgkmcnt(0)"
-               : "+v"(f[0].lo), "+v"(f[0].hi), "+v"(f[1].lo), "+v"(f[1].hi), "+v"(f[2].lo), "+v"(f[2].hi),
-                 "+v"(f[3].lo), "+v"(f[3].hi));
+__device__ __forceinline__ void read_fragments(const uint32_t (&at)[2], Fragment (&f)[2][2]) {
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:1024\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:8192\n\tds_read_b64_tr_b16 %5, %8 offset:9216\n\t"
+      "ds_read_b64_tr_b16 %6, %9 offset:8192\n\tds_read_b64_tr_b16 %7, %9 offset:9216\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0][0].lo), "=&v"(f[0][0].hi), "=&v"(f[0][1].lo), "=&v"(f[0][1].hi), "=&v"(f[1][0].lo),
+        "=&v"(f[1][0].hi), "=&v"(f[1][1].lo), "=&v"(f[1][1].hi)
+      : "v"(at[0]), "v"(at[1])
+      : "memory");
 }
 // A 16-byte LDS write.  Inline assembly, because before an ordinary one the
 // compiler waits for every LDS-bound load in flight; the next lds_barrier()
@@ -150,10 +166,13 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   auto zero_tail = [&](int slot, int step) {
     const int left = rows_left(step);
     if (left == kStep) return;
-    lds_char *const st = dy_lds + slot * kDyBytes + wn * 1024 + lane * 16;
+    // opaque: nothing is kept live across the loop for this
+    int l = lane_index();
+    asm volatile("" : "+v"(l));
+    lds_char *const st = dy_lds + slot * kDyBytes + wn * 1024 + l * 16;
 #pragma unroll
     for (int j = 0; j < kDyLoads; ++j)
-      if (drow + 16 * (j & 3) >= left) *(lds_u32x4 *)(st + j * 4096) = u32x4{0, 0, 0, 0};
+      if (4 * wn + (l >> 4) + 16 * (j & 3) >= left) *(lds_u32x4 *)(st + j * 4096) = u32x4{0, 0, 0, 0};
   };
 
   // x: a thread of half 0 takes FM columns (a run) by eight rows of t (a group:
@@ -163,14 +182,22 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   constexpr int kWords = FM / 4;
   typedef uint32_t Run __attribute__((ext_vector_type(kWords)));
   typedef __attribute__((address_space(1))) Run g_Run;
-  const int run = tid & 31, group = (tid & 255) >> 5;
   const int64_t t4 = (p.rows + 3) & ~static_cast<int64_t>(3);
-  const uint32_t xcol =
-      min(static_cast<uint32_t>(FM * run), static_cast<uint32_t>(min(p.kp - FM - k0, static_cast<int64_t>(TK))));
-  const uint32_t scol = xcol / kQ8Block * static_cast<uint32_t>(t4);
+  const uint32_t last_col = static_cast<uint32_t>(min(p.kp - FM - k0, static_cast<int64_t>(TK)));
+  // made anew where they are used: registers are short
+  auto run_and_group = [&](int &run, int &group) {
+    int l = lane_index();
+    asm volatile("" : "+v"(l));
+    run = l & 31;
+    group = 2 * wn + (l >> 5);
+  };
   Run codes[8];
   uint32_t sword[2];
   auto load_x = [&](int step) {
+    int run, group;
+    run_and_group(run, group);
+    const uint32_t xcol = min(static_cast<uint32_t>(FM * run), last_col);
+    const uint32_t scol = xcol / kQ8Block * static_cast<uint32_t>(t4);
     const int64_t t0 = static_cast<int64_t>(step) * kStep;
     const uint8_t *const xs = p.x + t0 * p.kp + k0, *const ss = p.sx + k0 / kQ8Block * t4 + t0;
     // Rows behind the last are loaded as copies of it, with scales of other
@@ -184,16 +211,15 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
     for (int h = 0; h < 2; ++h)
       sword[h] = *(const g_u32 *)(ss + (scol + static_cast<uint32_t>(min(group * 8 + 4 * h, last_word))));
   };
-  // where a thread's first column goes in LDS; its others follow 16 rows apart
-  uint32_t x_at;
-  {
-    const int r = run & 15, row = (r & 3) * 4 + (r >> 2);
-    x_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) +
-           static_cast<uint32_t>(((run >> 4) * (TK / 2) + row) * 128 + ((group ^ (row >> 1) ^ (row & 1)) & 7) * 16);
-  }
-  // expands and transposes the loaded codes into stage `slot`
+  // expands and transposes the loaded codes into stage `slot`: a thread's first
+  // column goes to `at`, its others follow 16 rows apart
   auto write_x = [&](int slot) {
-    const uint32_t at = x_at + static_cast<uint32_t>(slot * kXBytes);
+    int run, group;
+    run_and_group(run, group);
+    const int r = run & 15, row = (r & 3) * 4 + (r >> 2);
+    const uint32_t at =
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + static_cast<uint32_t>(slot * kXBytes) +
+        static_cast<uint32_t>(((run >> 4) * (TK / 2) + row) * 128 + ((group ^ (row >> 1) ^ (row & 1)) & 7) * 16);
     // half the scales (the bytes are 10 or more, but for those behind the last
     // row, which are the word's last)
     const uint32_t half[2] = {sword[0] - 0x01010101u, sword[1] - 0x01010101u};
@@ -235,7 +261,7 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
   const int full_steps = static_cast<int>(p.rows / kStep);
   auto zero_x_tail = [&](int slot, int step) {
     if (step < full_steps) return;
-    // opaque: no address is kept live across the loop for this
+    // opaque: nothing is kept live across the loop for this
     int l = lane_index();
     asm volatile("" : "+v"(l));
     for (int g = 2 * wn; g < 2 * wn + 2; ++g) {
@@ -263,11 +289,10 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
     const int row = 8 * (l >> 4) + ((l >> 2) & 3);
     return static_cast<uint32_t>(row * 256 + (l & 1) * 8 + ((((l & 3) >> 1) ^ swz(row)) * 16));
   };
-  auto read_dy = [&](const lds_char *op, uint32_t rb, int col, int s, Fragment &f) {
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(op)) +
-                        static_cast<uint32_t>((col >> 7) * kHalfBytes + s * (32 * 256)) + (rb ^ ((col & 127) * 2));
-    f.lo = read_transposed(at);
-    f.hi = read_transposed(at + 4 * 256);
+  static_assert(kHalfBytes == 16384 && 4 * 256 == 1024 && 32 * 256 == 8192, "offsets in read_fragments");
+  auto dy_at = [&](const lds_char *op, uint32_t rb, int col) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(op)) + static_cast<uint32_t>((col >> 7) * kHalfBytes) +
+           (rb ^ ((col & 127) * 2));
   };
   // x's fragments: row lane % 16 of block i, chunk 4 s + lane / 16
   auto x_base = [](int l) {
@@ -312,13 +337,10 @@ __device__ __forceinline__ void q8_wgrad_tile(lds_char *const lds, const Q8Weigh
 #pragma unroll
       for (int i = 0; i < FM; ++i) fx[s][i] = read_x(xs, xb, i, s);
     __builtin_amdgcn_sched_barrier(0);
+    uint32_t at[FN];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) read_dy(ds, rb, wn * (TN / 4) + j * 16, s, fd[s][j]);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_fragments(fd[0]);
-    wait_fragments(fd[1]);
+    for (int j = 0; j < FN; ++j) at[j] = dy_at(ds, rb, wn * (TN / 4) + j * 16);
+    read_fragments(at, fd);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (H == 1) {
       // dy of t + 1: all loads but those of t + 2
