@@ -43,12 +43,21 @@ def _stream_handle(device, stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+_raw = None
+
+
 def _raw_stream(index: int) -> int:
     """The handle of a device's current stream.  PyTorch has it without a
     Stream object around it, a microsecond and a half cheaper."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    global _raw
+    if _raw is None:
+        import torch
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw(index)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _allocating(stream):
@@ -56,8 +65,10 @@ def _allocating(stream):
     PyTorch's caching allocator hands a freed block out again at once to the
     stream that it belongs to, whose work is in order.  Kernels on another stream
     would write such a block while earlier work of its own may still use it."""
+    if stream is None:
+        return _NO_CONTEXT
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _capturing(device, stream) -> bool:
@@ -203,20 +214,18 @@ class Workspace:
         """At least ``nbytes`` on ``device``, for a call on ``stream`` (None:
         the device's current one)."""
         import torch
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
-            self.buf = None
+        handle = stream.cuda_stream if stream is not None else _raw_stream(device.index)
+        buf = self.buf
+        if buf is None or buf.numel() < nbytes or buf.device != device:
+            self.buf = buf = None
             with _allocating(stream):
-                self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            self._owner = self._handle(device, stream)
-        elif self._handle(device, stream) != self._owner:
-            _mark_used(stream if stream is not None else torch.cuda.current_stream(device), self.buf)
-        if _capturing(device, stream) and not any(b is self.buf for b in self._captured):
-            self._captured.append(self.buf)
-        return self.buf
-
-    @staticmethod
-    def _handle(device, stream) -> int:
-        return stream.cuda_stream if stream is not None else _raw_stream(device.index)
+                self.buf = buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self._owner = handle
+        elif handle != self._owner:
+            _mark_used(stream if stream is not None else torch.cuda.current_stream(device), buf)
+        if _capturing(device, stream) and not any(b is buf for b in self._captured):
+            self._captured.append(buf)
+        return buf
 
 
 def muon_step(params: Sequence, grads: Sequence, momenta: Sequence, scales: Sequence[float],

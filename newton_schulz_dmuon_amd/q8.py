@@ -122,8 +122,10 @@ def _check_rows(q: Q8Rows, rows: int) -> None:
 def _check_untracked(t, what: str) -> None:
     """No result carries a gradient on: an input that autograd tracks would leave
     its graph without a word."""
+    if not t.requires_grad:
+        return
     import torch
-    if t.requires_grad and torch.is_grad_enabled():
+    if torch.is_grad_enabled():
         raise _invalid(f"{what} requires a gradient, which this call does not record; call it under "
                        "torch.no_grad(), in an autograd.Function or on a detached tensor")
 
@@ -158,35 +160,37 @@ def _run(fn, device, stream, *args) -> None:
 
 
 def _check_stream(device, stream) -> None:
-    if stream is not None and stream.device != device:
+    if stream.device != device:
         raise _invalid(f"the stream is on {stream.device}, the tensors on {device}")
 
 
-def _keep(device, stream, made=(), given=()) -> None:
+def _keep(device, stream, results, made: bool, inputs) -> None:
     """For a call on a stream of its own: the memory of every tensor of it stays
     theirs until the stream is done with it, and that of results made for the
     call (which belongs to ``stream``) until the current stream is."""
     import torch
-    if stream is not None:
-        _mark_used(torch.cuda.current_stream(device), *made)
-        _mark_used(stream, *given)
+    _mark_used(stream, *results, *inputs)
+    if made:
+        _mark_used(torch.cuda.current_stream(device), *results)
 
 
 def q8_quantize(x, out: Optional[Q8Rows] = None, stream=None) -> Q8Rows:
     """8-bit rows of ``x`` (bf16 or fp32, ``[..., cols]``; the leading
     dimensions are flattened), one scale per 1 x 128 block."""
     device, rows, cols = _matrix(x, "x")
-    _check_stream(device, stream)
+    if stream is not None:
+        _check_stream(device, stream)
     dt = _dtype_code(x)
-    if out is None:
+    made = out is None
+    if made:
         with _allocating(stream):
             out = Q8Rows.empty(rows, cols, device)
-        _keep(device, stream, made=(out.codes, out.scales))
     else:
         if out.cols != cols or out.codes.device != device:
             raise _invalid("out does not fit x")
         _check_rows(out, rows)
-    _keep(device, stream, given=(x, out.codes, out.scales))
+    if stream is not None:
+        _keep(device, stream, (out.codes, out.scales), made, (x,))
     _run(load().dmuon_q8_quantize, device, stream, _ptr(x), dt, rows, cols, out.codes.data_ptr(),
          out.scales.data_ptr())
     return out
@@ -212,12 +216,12 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
             raise _invalid(f"matrix {i} is not 2-D")
         if not p.is_cuda or p.device != device:
             raise _invalid(f"matrix {i} is on {p.device}, not on {device} (a GPU)")
-    _check_stream(device, stream)
-    if out is None:
+    if stream is not None:
+        _check_stream(device, stream)
+    made = out is None
+    if made:
         with _allocating(stream):
             out = [Q8Weight.empty(p.shape[0], p.shape[1], device, transposed) for p in params]
-        for q in out:
-            _keep(device, stream, made=(q.codes, q.scales, q.codes_t, q.scales_t))
     else:
         out = list(out)
         if len(out) != n:
@@ -238,7 +242,8 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
         arr[i] = Q8WeightDesc(_ptr(p), _dtype_code(p), 0, p.shape[0], p.shape[1],
                               q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.codes_t),
                               _ptr(q.scales_t))
-        _keep(device, stream, given=(p, q.codes, q.scales, q.codes_t, q.scales_t))
+        if stream is not None:
+            _keep(device, stream, (q.codes, q.scales, q.codes_t, q.scales_t), made, (p,))
     _run(load().dmuon_q8_quantize_weights, device, stream, arr, n)
     for p, q in zip(params, out):
         q.rows, q.cols = p.shape
@@ -252,7 +257,12 @@ def _workspace(call, sizes, workspace: Optional[Workspace], device, stream):
     check(call(*sizes, ctypes.byref(need)))
     if need.value == 0:
         return None, 0, None
-    buf = (workspace or Workspace()).get(need.value, device, stream)
+    if workspace is not None:
+        buf = workspace.get(need.value, device, stream)
+    else:
+        import torch
+        with _allocating(stream):
+            buf = torch.empty(need.value, dtype=torch.uint8, device=device)
     return buf.data_ptr(), buf.numel(), buf
 
 
@@ -275,7 +285,8 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
     outs, inner = (w.cols, w.rows) if transpose else (w.rows, w.cols)
     if not a.codes.is_cuda:
         raise _invalid(f"codes are on {device}, not on a GPU")
-    _check_stream(device, stream)
+    if stream is not None:
+        _check_stream(device, stream)
     if a.cols != inner:
         raise _invalid(f"rows of {a.cols} columns against a weight of {inner}")
     _check_rows(a, rows)
@@ -283,10 +294,10 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
     _check_tensor(codes, "the weight's codes", (outs, kp), torch.float8_e4m3fn, device)
     _check_tensor(scales, "the weight's scales", (_up(outs, BLOCK) // BLOCK, kp // BLOCK),
                   torch.uint8, device)
-    if out is None:
+    made = out is None
+    if made:
         with _allocating(stream):
             out = torch.empty(rows, outs, dtype=dtype or torch.bfloat16, device=device)
-        _keep(device, stream, made=(out,))
     else:
         if dtype is not None and dtype != out.dtype:
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
@@ -297,7 +308,8 @@ def q8_matmul(a: Q8Rows, w: Q8Weight, transpose: bool = False, out=None, dtype=N
         dt |= _lib.Q8_FAST_SUMS
     ws, nws, keep = _workspace(lib.dmuon_q8_matmul_workspace_bytes, (rows, outs, inner, dt),
                                workspace, device, stream)
-    _keep(device, stream, given=(a.codes, a.scales, codes, scales, out))
+    if stream is not None:
+        _keep(device, stream, (out,), made, (a.codes, a.scales, codes, scales))
     _run(lib.dmuon_q8_matmul, device, stream, a.codes.data_ptr(), a.scales.data_ptr(), rows,
          codes.data_ptr(), scales.data_ptr(), outs, inner, out.data_ptr(), dt, ws, nws)
     return out
@@ -313,7 +325,8 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
     the gradient in place."""
     import torch
     device, rows, outs = _matrix(dy, "dy")
-    _check_stream(device, stream)
+    if stream is not None:
+        _check_stream(device, stream)
     if dy.dtype != torch.bfloat16:
         raise DmuonError(_lib.ERR_UNSUPPORTED_DTYPE, f"dy has dtype {dy.dtype}, not torch.bfloat16")
     if not dy.is_contiguous():
@@ -322,11 +335,11 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
         raise _invalid(f"codes are on {x.codes.device}, not on {device}")
     _check_rows(x, rows)
     cols = x.cols
-    if out is None:
+    made = out is None
+    if made:
         with _allocating(stream):
             out = torch.empty(outs, cols, device=device,
                               dtype=dtype or (base.dtype if base is not None else torch.bfloat16))
-        _keep(device, stream, made=(out,))
     else:
         if dtype is not None and dtype != out.dtype:
             raise _invalid(f"out has dtype {out.dtype}, not {dtype}")
@@ -337,7 +350,8 @@ def q8_weight_grad(dy, x: Q8Rows, out=None, dtype=None, base=None,
     lib = load()
     ws, nws, keep = _workspace(lib.dmuon_q8_weight_grad_workspace_bytes, (rows, outs, cols),
                                workspace, device, stream)
-    _keep(device, stream, given=(dy, x.codes, x.scales, base, out))
+    if stream is not None:
+        _keep(device, stream, (out,), made, (dy, x.codes, x.scales, base))
     _run(lib.dmuon_q8_weight_grad, device, stream, dy.data_ptr(), x.codes.data_ptr(),
          x.scales.data_ptr(), rows, outs, cols, base.data_ptr() if base is not None else None,
          out.data_ptr(), _dtype_code(out), ws, nws)
