@@ -23,18 +23,17 @@
 namespace dmuon {
 
 namespace {
-thread_local std::string g_last_error;
+// A plain buffer: a failed allocation can be reported, too.
+thread_local char g_last_error[512];
 }  // namespace
 
-void clear_error() { g_last_error.clear(); }
+void clear_error() { g_last_error[0] = '\0'; }
 
 int fail(int status, const char *fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return status;
 }
 
@@ -1289,11 +1288,11 @@ const char *dmuon_error_string(int status) {
   }
 }
 
-const char *dmuon_last_error(void) { return g_last_error.c_str(); }
+const char *dmuon_last_error(void) { return g_last_error; }
 
 int dmuon_partition_lpt(const int64_t *numel, int32_t n, int32_t n_owners, int32_t *owner_out,
                         int64_t *load_out) {
-  g_last_error.clear();
+  clear_error();
   if (n < 0) return fail(DMUON_ERR_INVALID_ARG, "n < 0");
   if (n_owners < 1) return fail(DMUON_ERR_INVALID_ARG, "n_owners < 1");
   if (n > 0 && (!numel || !owner_out)) return fail(DMUON_ERR_INVALID_ARG, "NULL array");
@@ -1326,7 +1325,7 @@ int dmuon_partition_lpt(const int64_t *numel, int32_t n, int32_t n_owners, int32
 
 int dmuon_pack_offsets(const int64_t *numel, int32_t n, int64_t align, int64_t *offset_out,
                        int64_t *total_out) {
-  g_last_error.clear();
+  clear_error();
   if (n < 0 || align < 1) return fail(DMUON_ERR_INVALID_ARG, "n < 0 or align < 1");
   if (!total_out || (n > 0 && (!numel || !offset_out)))
     return fail(DMUON_ERR_INVALID_ARG, "NULL array");
@@ -1343,7 +1342,7 @@ int dmuon_pack_offsets(const int64_t *numel, int32_t n, int64_t align, int64_t *
 
 int dmuon_nonfinite_flags_offset(const dmuon_matrix *mats, int32_t n, const dmuon_step_config *cfg,
                                  size_t *offset_out) {
-  g_last_error.clear();
+  clear_error();
   if (!offset_out) return fail(DMUON_ERR_INVALID_ARG, "offset_out is NULL");
   int rc = validate_config(cfg);
   if (rc) return rc;
@@ -1361,7 +1360,7 @@ int dmuon_nonfinite_flags_offset(const dmuon_matrix *mats, int32_t n, const dmuo
 
 int dmuon_chain_status_offset(const dmuon_matrix *mats, int32_t n, const dmuon_step_config *cfg,
                               size_t *offset_out) {
-  g_last_error.clear();
+  clear_error();
   if (!offset_out) return fail(DMUON_ERR_INVALID_ARG, "offset_out is NULL");
   int rc = validate_config(cfg);
   if (rc) return rc;
@@ -1381,7 +1380,7 @@ int dmuon_chain_status_offset(const dmuon_matrix *mats, int32_t n, const dmuon_s
 
 int dmuon_workspace_bytes(const dmuon_matrix *mats, int32_t n, const dmuon_step_config *cfg,
                           size_t *out_bytes) {
-  g_last_error.clear();
+  clear_error();
   if (!out_bytes) return fail(DMUON_ERR_INVALID_ARG, "out_bytes is NULL");
   int rc = validate_config(cfg);
   if (rc) return rc;
@@ -1403,7 +1402,7 @@ static int muon_step_impl(const dmuon_matrix *mats, int32_t n, const dmuon_step_
                           void *const *events, int32_t n_events, void *packed = nullptr,
                           int32_t packed_dtype = DMUON_BF16, int64_t packed_numel = 0,
                           bool noalloc = false) {
-  g_last_error.clear();
+  clear_error();
   if (n_events < 0 || (n_events > 0 && !events))
     return fail(DMUON_ERR_INVALID_ARG, "bad event list");
   if (packed) {
@@ -1565,7 +1564,7 @@ static int muon_step_impl(const dmuon_matrix *mats, int32_t n, const dmuon_step_
 
 int dmuon_step_launches(const dmuon_matrix *mats, int32_t n, const dmuon_step_config *cfg,
                         dmuon_launch_info *out, int32_t cap, int32_t *count) {
-  g_last_error.clear();
+  clear_error();
   if (!count) return fail(DMUON_ERR_INVALID_ARG, "count is NULL");
   if (cap < 0 || (cap > 0 && !out)) return fail(DMUON_ERR_INVALID_ARG, "bad output array");
   int rc = validate_config(cfg);
@@ -1608,7 +1607,7 @@ int dmuon_muon_step_packed(const dmuon_matrix *mats, int32_t n, const dmuon_step
                            int32_t packed_dtype, int64_t packed_numel, void *stream,
                            void *const *events, int32_t n_events) {
   if (!packed) {
-    g_last_error.clear();
+    clear_error();
     return fail(DMUON_ERR_INVALID_ARG, "packed is NULL");
   }
   return muon_step_impl(mats, n, cfg, workspace, workspace_bytes, stream, events, n_events, packed,
@@ -1623,7 +1622,7 @@ int dmuon_muon_step_noalloc(const dmuon_matrix *mats, int32_t n, const dmuon_ste
 // ------------------------------------------------------------------ AdamW --
 int dmuon_adamw_step(const dmuon_tensor *tensors, int32_t n, const dmuon_adamw_config *cfg,
                      void *stream) {
-  g_last_error.clear();
+  clear_error();
   if (!cfg) return fail(DMUON_ERR_INVALID_ARG, "cfg is NULL");
   const float vals[] = {cfg->lr, cfg->beta1, cfg->beta2, cfg->eps, cfg->weight_decay};
   for (float v : vals)
@@ -1697,7 +1696,7 @@ int dmuon_adamw_step(const dmuon_tensor *tensors, int32_t n, const dmuon_adamw_c
 static int pack_common(const dmuon_matrix *mats, int32_t n, int32_t field, void *packed_rw,
                        const void *packed, int32_t packed_dtype, int64_t packed_numel,
                        void *stream, bool to_packed) {
-  g_last_error.clear();
+  clear_error();
   if (n < 0) return fail(DMUON_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return DMUON_OK;
   if (!mats || !packed) return fail(DMUON_ERR_INVALID_ARG, "NULL mats or packed");

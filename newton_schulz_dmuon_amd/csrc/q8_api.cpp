@@ -81,7 +81,7 @@ int guarded(F f) {
   } catch (const std::exception &e) {
     return fail(DMUON_ERR_INVALID_ARG, "internal error: %s", e.what());
   } catch (...) {
-    return DMUON_ERR_INVALID_ARG;
+    return fail(DMUON_ERR_INVALID_ARG, "internal error");
   }
 }
 
