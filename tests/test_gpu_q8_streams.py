@@ -188,3 +188,49 @@ def test_a_captured_workspace_outlives_a_larger_call():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want) and all((h == 7).all() for h in held)
+
+
+def test_no_rows_on_another_stream():
+    print("no rows on a stream", flush=True)
+    s = torch.cuda.Stream()
+    w8 = nsd.q8_quantize_weights([torch.ones(130, 200, dtype=BF16, device="cuda")], stream=s)[0]
+    x8 = nsd.q8_quantize(torch.empty(0, 200, dtype=BF16, device="cuda"), stream=s)
+    assert nsd.q8_matmul(x8, w8, stream=s).shape == (0, 130)
+    grad = nsd.q8_weight_grad(torch.empty(0, 130, dtype=BF16, device="cuda"), x8, stream=s)
+    torch.cuda.synchronize()
+    assert grad.shape == (130, 200) and not grad.any()
+
+
+def test_a_capture_that_forks():
+    """A backward pass captured with the weight's gradient on a stream of its own,
+    nothing passed in and the temporaries dropped, replayed on changing inputs
+    beside eager calls."""
+    print("a forked capture", flush=True)
+    t, n, k = 2048, 384, 1536
+    x, dy, w, _ = layer_inputs(60, t, n, k)
+    s = torch.cuda.Stream()
+
+    def backward(x, dy, w, stream):
+        x8, w8 = nsd.q8_quantize(x), nsd.q8_quantize_weights([w])[0]
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        dx = nsd.q8_matmul(nsd.q8_quantize(dy), w8, transpose=True)
+        dw = nsd.q8_weight_grad(dy, x8, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        return dx, dw
+
+    backward(x, dy, w, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, dw = backward(x, dy, w, s)
+    for i in range(4):
+        nx, ndy, nw, _ = layer_inputs(61 + i, t, n, k)
+        x.copy_(nx)
+        dy.copy_(ndy)
+        w.copy_(nw)
+        graph.replay()
+        want = backward(nx, ndy, nw, None)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]), i
