@@ -94,7 +94,8 @@ constexpr int stream_ahead(int nt, int nn, int waves) { return waves == 8 || nt 
 // once, the rows' from L2 once per 16 NN outputs.  Rows and outputs behind the
 // last are clamped for the loads and not stored.  Column r of row block j is row
 // r * NT + j, so that a lane's NT scale bytes are one LDS word.
-// One row of a 14336 x 4096 weight takes 12.3 to 13.5 us, 4.4 to 4.8 TB/s (HBM).
+// One row of a 14336 x 4096 weight takes 14 us out of HBM, 4.2 TB/s, and 12.5
+// where the memory-side cache holds part of it; of a 4096 x 14336 one 12.5 to 13.
 template <int NT, int NN, int WAVES, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
   constexpr int kAhead = stream_ahead(NT, NN, WAVES);
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(WAVES * 64) void q8_stream_kernel(Q8Product p) {
 //
 // Bound by the matrix cores at the clock they leave: with fp32 sums, which
 // multiply in bf16 and expand in the same phase, 8192 rows of a 14336 x 4096
-// weight take 646 to 659 us, 1.46 to 1.49 PFLOP/s, and 2001 rows by a transposed
+// weight take 641 to 659 us, 1.46 to 1.50 PFLOP/s, and 2001 rows by a transposed
 // 18944 x 3584 weight 210 to 218, 1.3 (a library bf16 product 1.38).  With fast
 // sums the first takes 351 to 381 us, 2.53 to 2.74 PFLOP/s (a library 8-bit
 // product with one scale 2.5).
@@ -484,8 +485,8 @@ struct Plan {
 // 14336 x 4096 weight: 21 us with 4 x 2 blocks a work-group, 39 with one, 25 in
 // tiles; of a 4096 x 14336 one: 20.5 with 2 x 2, 36 and 24.  Those are fast sums;
 // fp32 sums take 21.7, 40 and 28.4, and 20.9, 36 and 27: bound alike, so one
-// model serves both (over 12 shapes its choice is the best for fp32 sums in ten
-// and within 12%; 256 rows of a 4096 x 4096 weight 16.3 us, fast 13.6, in tiles
+// model serves both (over 12 shapes its choice is within 12% of the best for fp32
+// sums and within 16% for fast ones; 256 rows of a 4096 x 4096 weight 16.3 us, fast 13.6, in tiles
 // 21.7 and 18.6).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
