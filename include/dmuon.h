@@ -465,8 +465,8 @@ int dmuon_q8_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner,
  *              NULL if that is 0.  Work that may overlap (calls on two streams,
  *              a call and a replayed graph, two graphs) needs one each.
  * Errors: INVALID_ARG (NULL pointer, rows < 0 or > 2^29, outs or inner < 1 or
- * > 2^22, a buffer of more than 2^37 elements), UNSUPPORTED_DTYPE,
- * MISALIGNED, ALIAS (out or the workspace overlaps another buffer),
+ * > 2^22, a buffer of more than 2^37 elements), UNSUPPORTED_DTYPE (fast sums of
+ * an fp32 result, too), MISALIGNED, ALIAS (out or the workspace overlaps another buffer),
  * WORKSPACE_TOO_SMALL, HIP. */
 int dmuon_q8_matmul(const void *codes, const void *scales, int64_t rows,
                     const void *codes_b, const void *scales_b, int64_t outs,
@@ -480,8 +480,8 @@ int dmuon_q8_weight_grad_workspace_bytes(int64_t rows, int64_t outs, int64_t col
 
 /* out[o][k] = base[o][k] + sum_t dy[t][o] * x[t][k], t < rows, o < outs,
  * k < cols: the weight gradient dy^T x from the 8-bit rows (codes, scales) of
- * x that the forward pass kept.  dy is bf16, rows x outs; the codes' values are
- * exact in bf16; sums are fp32, rounded once to out_dtype.  out may be a grad
+ * x that the forward pass kept.  dy is bf16, rows x outs; products are exact,
+ * sums fp32, rounded once to out_dtype.  out may be a grad
  * buffer of the step (dmuon_matrix.grad).
  *   base       NULL (zero), or outs x cols in out_dtype; may be out itself,
  *              which adds a micro-batch to the gradient in place

@@ -214,6 +214,10 @@ class Workspace:
         """At least ``nbytes`` on ``device``, for a call on ``stream`` (None:
         the device's current one)."""
         import torch
+        if isinstance(device, str):
+            device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
         handle = stream.cuda_stream if stream is not None else _raw_stream(device.index)
         buf = self.buf
         if buf is None or buf.numel() < nbytes or buf.device != device:

@@ -485,9 +485,9 @@ struct Plan {
 // 14336 x 4096 weight: 21 us with 4 x 2 blocks a work-group, 39 with one, 25 in
 // tiles; of a 4096 x 14336 one: 20.5 with 2 x 2, 36 and 24.  Those are fast sums;
 // fp32 sums take 21.7, 40 and 28.4, and 20.9, 36 and 27: bound alike, so one
-// model serves both (over 12 shapes its choice is within 12% of the best for fp32
-// sums and within 16% for fast ones; 256 rows of a 4096 x 4096 weight 16.3 us, fast 13.6, in tiles
-// 21.7 and 18.6).
+// model serves both.  Over 12 shapes its choice is within 12% of the best for
+// fp32 sums and within 16% for fast ones (256 rows of a 4096 x 4096 weight 16.3
+// us and 13.6, in tiles 21.7 and 18.6).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
   const float bytes = static_cast<float>((16 * nn + std::min<int64_t>(16 * nt, rows)) * kp);

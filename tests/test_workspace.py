@@ -61,6 +61,13 @@ def test_memory_belongs_to_the_stream_that_uses_it(streams):
     assert ws.get(2000, DEVICE, s).owner is s
 
 
+def test_a_device_without_an_index_is_the_current_one(streams):
+    ws = api.Workspace()
+    buf = ws.get(1000, "cuda")
+    assert buf.numel() == 1000 and ws.get(1000, torch.device("cuda")) is buf
+    assert ws.get(1000, DEVICE) is buf and ws.get(1000, "cuda:0") is buf
+
+
 def test_other_streams_are_recorded(streams):
     s = Stream(2)
     ws = api.Workspace()
