@@ -493,6 +493,100 @@ int dmuon_q8_weight_grad(const void *dy, const void *codes, const void *scales,
                          void *out, int32_t out_dtype, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit block products: the same layers with microscaled 4-bit operands, at up
+ * to twice the 8-bit matrix rate and half the bytes.  Not on the DMuon pages.
+ *
+ * The format (OCP microscaling, MXFP4).  Values are E2M1 codes (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6; bit 3 is the sign), two to a byte, the first in the low four bits,
+ * with one power-of-two scale 2^e per block of 32 along the direction that a
+ * product sums over, held as the byte e + 127: value = code * 2^e.  e is the
+ * smallest integer with max|block| <= 6 * 2^e, clamped to [-125, 126]; a code is
+ * value * 2^-e rounded to nearest even, or by a given random byte n: with f the
+ * part of the step between the codes next to the value that lies below it, up
+ * (away from zero) iff f >= (255.5 - n) / 256.  Random bytes that take every value
+ * equally often so round without a bias, to within 1/512 of a step.  A block that
+ * holds a NaN or an infinity gets the scale byte 255 and zero codes: it is NaN, and
+ * so is every result that sums over it.  Products take no other bytes than 2 to
+ * 253 and 255.  A matrix x [rows][cols] has two forms:
+ *   codes [rows][cp / 2], cp = cols rounded up to 256, blocks along a row, zero
+ *   codes behind cols; scales [cp / 32][r16], r16 = rows rounded up to 16, the
+ *   bytes behind rows and those of blocks behind cols those of a zero block (2)
+ *   codes_t [cols][rp / 2], scales_t [rp / 32][c16]: the same of x transposed,
+ *   blocks along a column of x.  They are other codes than the first.
+ * Buffers: 16-byte aligned.  Each call only enqueues kernels and takes no
+ * host-side buffer along, so it can be captured into a graph.
+ */
+
+/* One matrix of dmuon_q4_quantize. */
+typedef struct {
+  const void *x;       /* rows x cols, dtype, read only                        */
+  int32_t dtype;       /* DMUON_BF16 or DMUON_F32                              */
+  int32_t reserved;    /* must be 0                                            */
+  int64_t rows, cols;  /* 0 .. 2^29 (2^22 with codes_t) and 1 .. 2^22          */
+  const void *random;  /* rows x cols bytes, read only; NULL: to nearest       */
+  void *codes, *scales;     /* written; both NULL: not made                    */
+  void *codes_t, *scales_t; /* written; both NULL: not made                    */
+} dmuon_q4_source;
+
+/* Quantises n matrices (n = 0 is a no-op, and so is a matrix of no rows):
+ * activations, output gradients, or the params a step has just updated.  With
+ * both forms the matrix is read once, and both use the same random bytes.
+ * Errors: INVALID_ARG (a matrix of more than 2^37 elements, its sides rounded up
+ * to 256; neither form asked for), UNSUPPORTED_DTYPE, MISALIGNED, ALIAS (a written
+ * buffer overlaps any other buffer of the call), HIP. */
+int dmuon_q4_quantize(const dmuon_q4_source *m, int32_t n, void *stream);
+
+/* The values of codes and scales, out [rows][cols] in dtype: exact, but for
+ * 4 * 2^126, which the largest values of bf16 and fp32 round to and which becomes
+ * infinite.  With a matrix's codes_t and scales_t: rows = its cols, cols = its
+ * rows.  rows = 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE, MISALIGNED, ALIAS, HIP. */
+int dmuon_q4_dequantize(const void *codes, const void *scales, int64_t rows,
+                        int64_t cols, void *out, int32_t dtype, void *stream);
+
+/* Bytes of device workspace dmuon_q4_matmul needs for these sizes (0 for many).
+ * Host-only. */
+int dmuon_q4_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner,
+                                    size_t *out_bytes);
+
+/* out[t][o] = base[t][o] + sum_k a[t][k] * b[o][k], t < rows, o < outs,
+ * k < inner, of 4-bit a (codes, scales) and b (codes_b, scales_b).  Products are
+ * exact, sums fp32, rounded once to out_dtype.
+ *   y = x w^T     x's and w's codes; inner = w's cols
+ *   dx = dy w     dy's codes and w's codes_t; inner = w's rows
+ *   dw = dy^T x   dy's codes_t and x's codes_t; rows = w's rows, outs = w's cols,
+ *                 inner = the tokens; out may be a grad buffer of the step
+ *                 (dmuon_matrix.grad)
+ *   base       NULL (zero), or rows x outs in out_dtype; may be out itself, which
+ *              adds to it in place
+ *   workspace  at least dmuon_q4_matmul_workspace_bytes(), 256-byte aligned;
+ *              NULL if that is 0.  Work that may overlap (calls on two streams,
+ *              a call and a replayed graph, two graphs) needs one each.
+ * rows = 0 is a no-op; inner = 0: out = base, or zero (the operands may be NULL).
+ * Errors: INVALID_ARG (NULL pointer, rows < 0 or > 2^29, outs < 1 or > 2^22,
+ * inner < 0 or > 2^22, a buffer of more than 2^37 elements), UNSUPPORTED_DTYPE,
+ * MISALIGNED, ALIAS (out or the workspace overlaps another buffer),
+ * WORKSPACE_TOO_SMALL, HIP. */
+int dmuon_q4_matmul(const void *codes, const void *scales, int64_t rows,
+                    const void *codes_b, const void *scales_b, int64_t outs,
+                    int64_t inner, const void *base, void *out, int32_t out_dtype,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace dmuon_q4_rows_matmul needs for these sizes (0 for
+ * many).  Host-only. */
+int dmuon_q4_rows_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner,
+                                         size_t *out_bytes);
+
+/* dmuon_q4_matmul with bf16 rows x [rows][inner] in place of 4-bit ones and no
+ * base: a layer whose weight alone is held in 4 bits.  Products are exact, sums
+ * fp32, rounded once to out_dtype.  inner >= 1.
+ * Errors: those of dmuon_q4_matmul. */
+int dmuon_q4_rows_matmul(const void *x, int64_t rows, const void *codes_b,
+                         const void *scales_b, int64_t outs, int64_t inner,
+                         void *out, int32_t out_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

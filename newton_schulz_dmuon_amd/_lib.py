@@ -47,7 +47,9 @@ EXPORTED = ("dmuon_abi_version", "dmuon_error_string", "dmuon_last_error",
             "dmuon_nonfinite_flags_offset", "dmuon_muon_step_noalloc",
             "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
             "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
-            "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad")
+            "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad",
+            "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
+            "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul")
 
 # DMUON_NOALLOC_SCRATCH_BYTES
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -121,6 +123,22 @@ class Q8WeightDesc(ctypes.Structure):
     ]
 
 
+class Q4SourceDesc(ctypes.Structure):
+    """``dmuon_q4_source``"""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("random", ctypes.c_void_p),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("codes_t", ctypes.c_void_p),
+        ("scales_t", ctypes.c_void_p),
+    ]
+
+
 class DmuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"dmuon status {status}: {message}")
@@ -175,13 +193,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dmuon_q8_weight_grad_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
     lib.dmuon_q8_weight_grad.argtypes = [vp, vp, vp, c_i64, c_i64, c_i64, vp, vp, c_i32, vp, size_t,
                                          vp]
+    lib.dmuon_q4_quantize.argtypes = [P(Q4SourceDesc), c_i32, vp]
+    lib.dmuon_q4_dequantize.argtypes = [vp, vp, c_i64, c_i64, vp, c_i32, vp]
+    lib.dmuon_q4_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
+    lib.dmuon_q4_matmul.argtypes = [vp, vp, c_i64, vp, vp, c_i64, c_i64, vp, vp, c_i32, vp, size_t, vp]
+    lib.dmuon_q4_rows_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
+    lib.dmuon_q4_rows_matmul.argtypes = [vp, c_i64, vp, vp, c_i64, c_i64, vp, c_i32, vp, size_t, vp]
     for name in ("dmuon_partition_lpt", "dmuon_pack_offsets", "dmuon_workspace_bytes",
                  "dmuon_pack", "dmuon_unpack", "dmuon_muon_step", "dmuon_muon_step_traced",
                  "dmuon_muon_step_packed", "dmuon_adamw_step", "dmuon_step_launches",
                  "dmuon_nonfinite_flags_offset", "dmuon_muon_step_noalloc",
                  "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
                  "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
-                 "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad"):
+                 "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad",
+            "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
+            "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.dmuon_abi_version() != ABI_VERSION:
         raise ImportError(f"libdmuon ABI {lib.dmuon_abi_version()} != {ABI_VERSION}")

@@ -17,10 +17,11 @@ Modules
 ``oracle.partition``  balanced (LPT greedy) owner assignment and pack offsets.
 ``oracle.adamw``      AdamW step for the parameters Muon does not own.
 ``oracle.q8``         the 8-bit block format and its products.
+``oracle.q4``         the 4-bit block format and its products.
 
 Every function is pinned by a ``-m "not gpu"`` test against something other
 than itself (closed forms, library routines, invariants, brute force).  No
 function is "parity unpinned".
 """
 
-from . import adamw, muon, pack, partition, q8  # noqa: F401
+from . import adamw, muon, pack, partition, q4, q8  # noqa: F401
