@@ -12,62 +12,241 @@
 // Weights b are the instruction's first operand and rows a the second: a lane
 // then holds four consecutive outputs of one row.
 
+#include <algorithm>
+
 #include "q4_device.h"
 
 namespace dmuon {
 
 namespace {
 
-constexpr int64_t kSide = 64;  // of a work-group's tile
+// ---- tiles: many rows ----
+//
+// One work-group of 8 waves (2 x 4) computes TA outputs of the weight by TB rows;
+// each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 64 elements per step: 128
+// bytes of a row, and a quarter of the 256 codes (128 bytes) that a stage of the
+// weight holds.  Both come into LDS by LDS-bound loads (16 bytes a lane, 128-byte
+// rows, the 16-byte chunk XORed with (row / 2) mod 8, which keeps the fragment reads
+// off each other's banks), in a ring of two stages each: a step loads the next
+// step's rows and a quarter of the next stage of the weight.  The two halves of the
+// work-group (wm) run in ping-pong: one half's waves read fragments and issue loads
+// while the other half's expand and multiply, switching at every barrier.
+//
+// A lane's 16 codes of a step are k = 16 g4 + 0 .. 15, eight of them an instruction.
+// The order of rows in LDS is that of the 4-bit product's tiles.
+constexpr int kTileThreads = 512;
+constexpr int kRowBytes = 128;
+constexpr int kStep = 64, kStageSteps = kQ4Pad / kStep;
+constexpr int kStageBlocks = kQ4Pad / kQ4Block;
 
-// A work-group of four waves (2 x 2) computes 64 outputs by 64 rows; rows and
-// outputs behind the last are clamped for the loads and not stored.
-__global__ __launch_bounds__(256) void q4_rows_tile_kernel(Q4Product p, uint32_t na) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g4 = lane >> 4;
-  const uint32_t tb = blockIdx.x / na;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * na) * kSide + (wave & 1) * 32;
-  const int64_t t0 = static_cast<int64_t>(tb) * kSide + (wave >> 1) * 32;
-  const int64_t rb = (p.outs + 15) / 16 * 16;
-  const int64_t n1[2] = {min(n0 + r16, p.outs - 1), min(n0 + 16 + r16, p.outs - 1)};
-  const int64_t t1[2] = {min(t0 + r16, p.rows - 1), min(t0 + 16 + r16, p.rows - 1)};
-  f32x4 acc[2][2] = {};
-  for (int64_t k = 0; k < p.kp; k += 32) {
-    const int64_t kl = k + g4 * 8;
-    bf16x8 fb[2], fa[2];
+// Rows as the kernels read them: ld elements apart, a multiple of kStep, zeros
+// behind the last.
+struct Rows {
+  const uint8_t *x;
+  int64_t ld;
+};
+
+template <int TA, int TB>
+__device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Product &p, const Rows &x, int64_t n0,
+                                             int64_t t0, int kbeg, int kend, f32x4 (&acc)[TA / 32][TB / 64]) {
+  constexpr int FM = TA / 32, FN = TB / 64;
+  // two stages of the weight with its scales (each half's [block][output]), two
+  // of the rows
+  constexpr int kScales = TA * kRowBytes, kWeight = kScales + TA * kStageBlocks, kRows = TB * kRowBytes;
+  lds_char *const lds_x = lds + 2 * kWeight;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
+  const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+
+  const uint8_t *const gb = p.b + n0 * kpb, *const ga = x.x + t0 * ldb;
+  // the last output and row of the tile that exist
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TA - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TB - 1)));
+  // scales: 16 outputs a lane, TA/32 lanes a block
+  const uint8_t *const gsb = p.sb + lane / (TA / 32) * rb + min(n0 + wm * (TA / 2) + lane % (TA / 32) * 16, rb - 16);
+  // loads: lane l of 1 KB load j of a half fills LDS row (j * 4 + wn) * 8 + l / 8,
+  // physical chunk l % 8
+  const int q = (wn & 1) * 8 + (lane >> 3);
+  const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (((wn & 1) * 4 + (lane >> 4)) & 7)) * 16;
+  const int base_n = ((q & 3) * 4 + (q >> 2)) * FM + (wn >> 1) + wm * (TA / 2);
+  const int base_t = q * FN + (wn >> 1);
+  auto piece = [&](const uint8_t *src, lds_char *to) {
+    __builtin_amdgcn_global_load_lds((const void *)src, (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+  };
+  auto load = [&](const uint8_t *src, int row, uint32_t bytes, lds_char *to) {
+    piece(src + (__umul24(static_cast<uint32_t>(row), bytes) + chunk), to + wn * 1024);
+  };
+  // part j (of kStageSteps) of this half's codes of stage kb, and their scales
+  auto issue_weight = [&](int kb, int j) {
+    lds_char *const st = lds + (kb & 1) * kWeight;
+    const int last = static_cast<int>(p.kp / kQ4Pad) - 1;
+    const int64_t k = min(kb, last);
+    if (j < TA / 64) load(gb + k * kRowBytes, min(base_n + 2 * j, lim_n), kpb, st + wm * (kScales / 2) + j * 4096);
+    if (j == kStageSteps - 1 && wn == 3 && lane < TA / 4)
+      piece(gsb + k * kStageBlocks * rb, st + kScales + wm * (TA / 2 * kStageBlocks));
+  };
+  auto issue_rows = [&](int slot, int ks) {
+    if (wm != 0) return;
+    lds_char *const st = lds_x + slot * kRows;
+    int bt = base_t;
+    // opaque: the offsets are rebuilt at every issue instead of being kept
+    // live across the loop
+    asm volatile("" : "+v"(bt));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w = *(const g_u32 *)(p.b + n1[i] * (p.kp / 2) + kl / 2);
-      fb[i] = q4_expand8(w, q4_half_scale(((const g_u8 *)p.sb)[k / kQ4Block * rb + n1[i]]));
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        fa[i][e] = kl + e < p.inner ? static_cast<__bf16>(load_elem(p.a, kBF16, t1[i] * p.inner + kl + e))
-                                    : static_cast<__bf16>(0.f);
+      for (int j = 0; j < TB / 64; ++j) {
+        // row s of the tile's LDS rows: quarter s / (TB / 4), then block and column
+        const int s = h * (TB / 2) + j * 32, in_quarter = s % (TB / 4);
+        const int row = s / (TB / 4) * (TB / 4) + in_quarter / 16;
+        load(ga + static_cast<int64_t>(ks) * kRowBytes, min(bt + row, lim_t), ldb, st + s * kRowBytes);
+      }
+  };
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int first = kbeg * kStageSteps;
+  const int end = min(kend * kStageSteps, static_cast<int>(x.ld / kStep));
+#pragma unroll
+  for (int j = 0; j < kStageSteps; ++j) issue_weight(kbeg, j);
+  issue_rows(first & 1, first);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (wm == 1) barrier();
+  for (int ks = first; ks < end; ++ks) {
+    const int kb = ks / kStageSteps, part = ks % kStageSteps;
+    const lds_char *const st = lds + (kb & 1) * kWeight;
+    const lds_char *const opb = st + wm * (kScales / 2);
+    const lds_char *const opa = lds_x + (ks & 1) * kRows + wn * (TB / 4 * kRowBytes);
+    // the last step loads its own rows again, into the free stage, which keeps the
+    // loop free of a branch
+    issue_rows((ks + 1) & 1, min(ks + 1, end - 1));
+    issue_weight(kb + 1, part);
+    u32x2 fb[FM];
+    u32x4 fa[FN][2];
+    uint32_t sb[FM / 4];
+    const int block = 2 * part + (g4 >> 1);
+    const lds_char *const ws = st + kScales + wm * (TA / 2 * kStageBlocks) + block * (TA / 2) + ((r16 & 3) * 4 + (r16 >> 2)) * FM;
+    if constexpr (FM == 8) {
+      const u32x2 w = *(const lds_u32x2 *)ws;
+      sb[0] = w.x;
+      sb[1] = w.y;
+    } else {
+      sb[0] = *(const lds_u32 *)ws;
     }
+    const uint32_t at_b = static_cast<uint32_t>(r16 * kRowBytes + ((block ^ (r16 >> 1)) & 7) * 16 + (g4 & 1) * 8);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < FM; ++i) fb[i] = *(const lds_u32x2 *)(opb + at_b + i * (16 * kRowBytes));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[i], fa[j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        fa[j][d] = *(const lds_u32x4 *)(opa + r16 * kRowBytes + (((2 * g4 + d) ^ (r16 >> 1)) & 7) * 16 + j * (16 * kRowBytes));
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const float s = q4_half_scale(sb[i / 4] >> (8 * (i % 4)) & 0xff);
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const bf16x8 xb = q4_expand8(fb[i][d], s);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, fa[j][d]), acc[i][j], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   }
+  if (wm == 0) barrier();
+}
+
+template <int TA, int TB>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TB == 256 ? 2 : 4)))
+void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
+  constexpr int FM = TA / 32, FN = TB / 64;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * (TA * (kRowBytes + kStageBlocks) + TB * kRowBytes)];
+  const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
+  const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
+  f32x4 acc[FM][FN];
+  q4_rows_tile<TA, TB>((lds_char *)smem, p, x, n0, t0, w.begin, w.end, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
+  const TileOut o = tile_out(w, TA, TB, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < FN; ++j) {
+    const int r = wn * (TB / 4) + r16 * FN + j;
+    if (r >= o.rows) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t t = t0 + j * 16 + r16, n = n0 + i * 16 + 4 * g4;
-      if (t >= p.rows) continue;
-      float v[4] = {2 * acc[i][j][0], 2 * acc[i][j][1], 2 * acc[i][j][2], 2 * acc[i][j][3]};
-      finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
+    for (int v = 0; v < 4; ++v) {
+      const int c = wm * (TA / 2) + (v * 4 + g4) * FM;
+      float run[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) run[i] = 2.f * acc[i][j][v];
+      finish_run<FM>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
+  }
+}
+
+constexpr std::initializer_list<TileCost> kCosts = {
+    {256, 256, 1, 4.5f, 5.8f}, {128, 256, 1, 2.8f, 3.4f}, {128, 128, 2, 1.9f, 3.8f}};
+
+// How a product runs: its tiles' split, and the bytes of its workspace's two
+// parts, the padded rows and the pieces' results.
+struct Plan {
+  TileSplit split;
+  int64_t ld;
+  size_t pad_bytes, piece_bytes;
+};
+
+Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
+  Plan pl{};
+  if (rows == 0) return pl;
+  pl.split = choose_split(outs, rows, (inner + kQ4Pad - 1) / kQ4Pad, kCosts);
+  pl.ld = (inner + kStep - 1) / kStep * kStep;
+  if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
+  pl.piece_bytes = pl.split.ws_bytes();
+  return pl;
+}
+
+template <int TA, int TB>
+hipError_t launch_tiles(const Q4Product &p, const Rows &x, const TileSplit &sp, hipStream_t st) {
+  hipLaunchKernelGGL((q4_rows_tile_kernel<TA, TB>), dim3(sp.whole + sp.tail * sp.pieces), dim3(kTileThreads), 0, st, p,
+                     x, sp);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t q4_rows_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t q4_rows_workspace(int64_t rows, int64_t outs, int64_t inner) {
+  const Plan pl = plan_of(rows, outs, inner);
+  return pl.pad_bytes + pl.piece_bytes;
+}
 
-hipError_t launch_q4_rows(const Q4Product &p, hipStream_t st) {
-  const int64_t na = (p.outs + kSide - 1) / kSide, nb = (p.rows + kSide - 1) / kSide;
-  hipLaunchKernelGGL(q4_rows_tile_kernel, dim3(static_cast<uint32_t>(na * nb)), dim3(256), 0, st, p,
-                     static_cast<uint32_t>(na));
-  return hipGetLastError();
+hipError_t launch_q4_rows(const Q4Product &args, hipStream_t st) {
+  Q4Product p = args;
+  const Plan pl = plan_of(p.rows, p.outs, p.inner);
+  Rows x{static_cast<const uint8_t *>(p.a), pl.ld};
+  if (pl.pad_bytes) {
+    const hipError_t e = launch_pad_rows(p.a, p.rows, p.inner, pl.ld, p.ws, st);
+    if (e != hipSuccess) return e;
+    x.x = static_cast<const uint8_t *>(p.ws);
+    p.ws = static_cast<char *>(p.ws) + pl.pad_bytes;
+  }
+  const TileSplit &sp = pl.split;
+  const hipError_t e = sp.ta == 256   ? launch_tiles<256, 256>(p, x, sp, st)
+                       : sp.tb == 256 ? launch_tiles<128, 256>(p, x, sp, st)
+                                      : launch_tiles<128, 128>(p, x, sp, st);
+  if (e != hipSuccess || sp.pieces == 1) return e;
+  return launch_q8_reduce(static_cast<const float *>(p.ws), sp, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
 }
 
 }  // namespace dmuon

@@ -90,6 +90,9 @@ struct Q8WeightGrad {
   int64_t dy_ld;          // set by the launcher
   int32_t out_dt;
 };
+// A copy of bf16 rows [rows][cols] as [rows][ld], zeros behind cols; ld is a
+// multiple of 8.
+hipError_t launch_pad_rows(const void *x, int64_t rows, int64_t cols, int64_t ld, void *out, hipStream_t st);
 size_t q8_wgrad_workspace(int64_t rows, int64_t outs, int64_t cols);
 hipError_t launch_q8_wgrad(const Q8WeightGrad &p, hipStream_t st);
 

@@ -462,10 +462,10 @@ __global__ __launch_bounds__(256) void q8_wgrad_empty_kernel(Q8WeightGrad p) {
   }
 }
 
-// A copy of dy with rows of a multiple of 8 elements (zeros behind the last
-// column), for a dy whose rows are not: the LDS-bound loads take 16 bytes.  One
-// pass, bound by HBM: 8192 x 14335 in about 95 us, beside 110 for the product
-// with 512 columns.
+// A copy of bf16 rows with rows of ld elements, a multiple of 8 (zeros behind the
+// last column), for a dy whose rows are no such multiple: the LDS-bound loads take
+// 16 bytes.  One pass, bound by HBM: 8192 x 14335 in about 95 us, beside 110 for
+// the product with 512 columns.
 __global__ __launch_bounds__(256) void q8_pad_rows_kernel(const uint16_t *__restrict__ dy, int64_t rows, int64_t cols,
                                                           int64_t ld, uint16_t *__restrict__ out) {
   for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; at < rows * ld;
@@ -516,6 +516,12 @@ size_t q8_wgrad_workspace(int64_t rows, int64_t outs, int64_t cols) {
   return pl.pad_bytes + pl.piece_bytes;
 }
 
+hipError_t launch_pad_rows(const void *x, int64_t rows, int64_t cols, int64_t ld, void *out, hipStream_t st) {
+  hipLaunchKernelGGL(q8_pad_rows_kernel, dim3(element_groups(rows * ld)), dim3(256), 0, st,
+                     static_cast<const uint16_t *>(x), rows, cols, ld, static_cast<uint16_t *>(out));
+  return hipGetLastError();
+}
+
 hipError_t launch_q8_wgrad(const Q8WeightGrad &args, hipStream_t st) {
   Q8WeightGrad p = args;
   if (p.rows == 0) {
@@ -525,9 +531,7 @@ hipError_t launch_q8_wgrad(const Q8WeightGrad &args, hipStream_t st) {
   const Plan pl = plan_of(p.rows, p.outs, p.cols);
   p.dy_ld = pl.dy_ld;
   if (pl.pad_bytes) {
-    hipLaunchKernelGGL(q8_pad_rows_kernel, dim3(element_groups(p.rows * pl.dy_ld)), dim3(256), 0, st,
-                       static_cast<const uint16_t *>(p.dy), p.rows, p.outs, pl.dy_ld, static_cast<uint16_t *>(p.ws));
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_pad_rows(p.dy, p.rows, p.outs, pl.dy_ld, p.ws, st);
     if (e != hipSuccess) return e;
     p.dy = p.ws;
     p.ws = static_cast<char *>(p.ws) + pl.pad_bytes;
