@@ -95,31 +95,32 @@ int dmuon_q4_quantize(const dmuon_q4_source *m, int32_t n, void *stream) {
     if ((rc = b.check())) return rc;
     Q4Batch batch;
     std::memset(&batch, 0, sizeof batch);
+    auto flush = [&]() -> int {
+      const int status = check_launch(launch_q4_quantize(batch, static_cast<hipStream_t>(stream)), "q4 quantise launch");
+      std::memset(&batch, 0, sizeof batch);
+      return status;
+    };
     for (int32_t i = 0; i < n; ++i) {
       const dmuon_q4_source &d = m[i];
-      if (d.rows > 0) {
-        const int k = batch.n;
-        batch.x[k] = d.x;
-        batch.random[k] = static_cast<const uint8_t *>(d.random);
-        batch.codes[k] = static_cast<uint8_t *>(d.codes);
-        batch.scales[k] = static_cast<uint8_t *>(d.scales);
-        batch.codes_t[k] = static_cast<uint8_t *>(d.codes_t);
-        batch.scales_t[k] = static_cast<uint8_t *>(d.scales_t);
-        batch.rows[k] = d.rows;
-        batch.cols[k] = d.cols;
-        batch.dt[k] = d.dtype;
-        // a matrix has at most 2^37 / 2^14 tiles, so a batch's threads stay
-        // below 2^32
-        batch.first_tile[k + 1] = batch.first_tile[k] + q4_tiles(d.rows, d.cols, d.codes != nullptr, d.codes_t != nullptr);
-        batch.n = k + 1;
-      }
-      if (batch.n == kQ4Batch || i + 1 == n || batch.first_tile[batch.n] > (1 << 22)) {
-        rc = check_launch(launch_q4_quantize(batch, static_cast<hipStream_t>(stream)), "q4 quantise launch");
-        if (rc) return rc;
-        std::memset(&batch, 0, sizeof batch);
-      }
+      if (d.rows == 0) continue;
+      // a matrix has at most 2^37 / 2^14 tiles, so a batch's threads stay below 2^32
+      if (batch.n > 0 && (batch.n == kQ4Batch || batch.first_tile[batch.n] > (1 << 22) || batch.dt != d.dtype ||
+                          !batch.random[0] != !d.random) &&
+          (rc = flush()))
+        return rc;
+      const int k = batch.n++;
+      batch.dt = d.dtype;
+      batch.x[k] = d.x;
+      batch.random[k] = static_cast<const uint8_t *>(d.random);
+      batch.codes[k] = static_cast<uint8_t *>(d.codes);
+      batch.scales[k] = static_cast<uint8_t *>(d.scales);
+      batch.codes_t[k] = static_cast<uint8_t *>(d.codes_t);
+      batch.scales_t[k] = static_cast<uint8_t *>(d.scales_t);
+      batch.rows[k] = d.rows;
+      batch.cols[k] = d.cols;
+      batch.first_tile[k + 1] = batch.first_tile[k] + q4_tiles(d.rows, d.cols, d.codes != nullptr, d.codes_t != nullptr);
     }
-    return DMUON_OK;
+    return batch.n > 0 ? flush() : DMUON_OK;
   });
 }
 

@@ -22,18 +22,18 @@ constexpr int kQ4MinExp = -125, kQ4MaxExp = 126;
 // is NaN.
 constexpr int kQ4Nan = 255;
 
-// Quantising: batches of up to kQ4Batch matrices per launch, by value.
+// Quantising: batches of up to kQ4Batch matrices of one type per launch, by value;
+// all of them rounded by random bytes, or none.
 constexpr int kQ4Batch = 24;
 struct Q4Batch {
   int32_t n;
-  int32_t pad_;
+  int32_t dt;
   int64_t first_tile[kQ4Batch + 1];  // prefix sum of 128 x 128 tiles
   const void *x[kQ4Batch];
   const uint8_t *random[kQ4Batch];                  // nullable
   uint8_t *codes[kQ4Batch], *scales[kQ4Batch];      // both null: not written
   uint8_t *codes_t[kQ4Batch], *scales_t[kQ4Batch];  // both null: not written
   int64_t rows[kQ4Batch], cols[kQ4Batch];
-  int32_t dt[kQ4Batch];
 };
 // Tiles of 128 x 128 that a matrix takes: over its elements, the padding of its
 // codes and that of its scale tables.

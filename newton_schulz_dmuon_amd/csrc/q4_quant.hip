@@ -23,6 +23,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
 
+// eight bytes at any address
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
+typedef __attribute__((address_space(1))) u32x2_at1 g_u32x2_at1;
+
 // The scale byte of a block whose largest magnitude has these fp32 bits.
 __device__ __forceinline__ int scale_byte(uint32_t amax) {
   if (amax >= 0x7f800000u) return kQ4Nan;
@@ -34,28 +38,90 @@ __device__ __forceinline__ int scale_byte(uint32_t amax) {
 // for kQ4Nan, with which every conversion from a code gives NaN.
 __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
 
-// |v| * 2^-e rounded by a random byte: up iff the part of a step that is left is
-// at least (255.5 - n) / 256, so by n + 0.5 of 256 equally likely cases.  All of
-// it is exact in fp32.
-__device__ __forceinline__ uint32_t random_code(float v, float inv, uint32_t n) {
-  const float a = __builtin_fabsf(v) * inv;
-  const float per = a < 2.f ? 2.f : a < 4.f ? 1.f : 0.5f;  // codes per unit
-  const float at = a * per, whole = __builtin_floorf(at);
-  // codes below 2, 4 and 6: 0 .. 3, 4 and 5, 6 and 7
-  const uint32_t first = a < 2.f ? 0u : a < 4.f ? 2u : 4u;
-  const uint32_t up = at - whole >= (255.5f - static_cast<float>(n)) * 0.00390625f ? 1u : 0u;
-  return (static_cast<uint32_t>(whole) + first + up) | (__float_as_uint(v) >> 31 << 3);
+// Eight elements as loaded: four words of bf16 pairs, or eight of fp32.
+template <bool F32> struct Eight {
+  uint32_t w[F32 ? 8 : 4];
+  // at any element's address, all loads before the first use
+  __device__ __forceinline__ void load(const void *x, int64_t i) {
+    if constexpr (F32) {
+      const u32x4 a = *(const g_u32x4_at4 *)(static_cast<const float *>(x) + i);
+      const u32x4 b = *(const g_u32x4_at4 *)(static_cast<const float *>(x) + i + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = a[k];
+        w[4 + k] = b[k];
+      }
+    } else {
+      const u32x4 a = *(const g_u32x4_at2 *)(static_cast<const uint16_t *>(x) + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = a[k];
+    }
+  }
+  // the first `left` of them, zeros behind
+  __device__ __forceinline__ void load_some(const void *x, int64_t i, int64_t left) {
+#pragma unroll
+    for (int k = 0; k < (F32 ? 8 : 4); ++k) w[k] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < left) {
+        if constexpr (F32)
+          w[k] = ((const g_u32 *)x)[i + k];
+        else
+          w[k / 2] |= static_cast<uint32_t>(((const g_u16 *)x)[i + k]) << (16 * (k % 2));
+      }
+  }
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (F32) return __uint_as_float(w[k]);
+    return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  }
+};
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// Magnitudes as ordered bits: fp32's, or two bf16's in the halves of a word.
+template <bool F32> __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & (F32 ? 0x7fffffffu : 0x7fff7fffu); }
+template <bool F32> __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (F32) return max(a, b);
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
-// The codes of eight elements, the first in the lowest four bits.
+// The larger of this lane's value and that of the lane DPP control CTRL names.
+template <bool F32, int CTRL>
+__device__ __forceinline__ uint32_t larger_dpp(uint32_t v) {
+  return larger<F32>(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true)));
+}
+// ... over the four lanes of a quad
+template <bool F32> __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  return larger_dpp<F32, 0x4e>(larger_dpp<F32, 0xb1>(v));
+}
+// ... over the lanes l, l + 4, l + 8 and l + 12 of a row of 16 (rotations by 4 and 8)
+template <bool F32> __device__ __forceinline__ uint32_t stride4_max(uint32_t v) {
+  return larger_dpp<F32, 0x128>(larger_dpp<F32, 0x124>(v));
+}
+
+// A value times 2^-e rounded by a random byte n: in units of 2^-10, of which a step
+// between codes has 512, 1024 or 2048 (values below 2, 4 and 6), up iff what lies
+// above the code below is at least 255.5 - n of 256 parts.  Cutting the value to
+// whole units changes no comparison, since every threshold is a whole number of
+// them.  unit: 2^(10 - e).
+__device__ __forceinline__ uint32_t random_code(float v, float unit, uint32_t n) {
+  const uint32_t u = static_cast<uint32_t>(__builtin_fabsf(v) * unit);
+  const uint32_t wide = min(u >> 11, 2u);
+  return ((u + ((2 * n + 1) << wide)) >> (9 + wide)) + 2 * wide;
+}
+
+// The codes of eight elements, the first in the lowest four bits.  n: their random
+// bytes.
 template <bool RANDOM>
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], int byte, const uint8_t (&n)[8]) {
-  if (byte == kQ4Nan) return 0;
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], int byte, u32x2 n) {
   uint32_t w = 0;
   if constexpr (RANDOM) {
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+    // 2^(10 - e) in two factors, of which fp32 holds each
+    const float unit = __uint_as_float(static_cast<uint32_t>(min(254 + 10 - byte, 254)) << 23);
+    const float more = byte < 10 ? __uint_as_float(static_cast<uint32_t>(127 + 10 - byte) << 23) : 1.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w |= random_code(v[k], inv, n[k]) << (4 * k);
+    for (int k = 0; k < 8; ++k)
+      w |= (random_code(v[k] * more, unit, n[k / 4] >> (8 * (k % 4)) & 0xff) | (__float_as_uint(v[k]) >> 31 << 3)) << (4 * k);
   } else {
     const float s = scale_of(byte);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
@@ -63,18 +129,8 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], int byte, const 
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
   }
-  return w;
+  return byte == kQ4Nan ? 0u : w;
 }
-
-// The larger of this lane's value and that of the lane DPP control CTRL names.
-template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true)));
-}
-// ... over the four lanes of a quad
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) { return max_dpp<0x4e>(max_dpp<0xb1>(v)); }
-// ... over the lanes l, l + 4, l + 8 and l + 12 of a row of 16 (rotations by 4 and 8)
-__device__ __forceinline__ uint32_t stride4_max(uint32_t v) { return max_dpp<0x128>(max_dpp<0x124>(v)); }
 
 // Eight scale bytes as two words.
 __device__ __forceinline__ u32x2 pack8(const int (&b)[8]) {
@@ -87,108 +143,154 @@ __device__ __forceinline__ u32x2 pack8(const int (&b)[8]) {
 // One tile of 128 x 128.  A lane holds an 8 x 8 patch; a quad's lanes lie side by
 // side along a row (a row's block of 32), the lanes 4 apart of a row of 16 below
 // each other (a column's block), the four rows of 16 cover 128 columns and the
-// four waves 128 rows.
+// four waves 128 rows.  Both directions' maxima are then taken by DPP alone.  The
+// transposed codes leave through LDS, 64 bytes of a column at a time.
+constexpr int kPitch = kTile / 2 + 4;  // bytes of a column in LDS
+
 template <bool F32, bool RANDOM>
-__device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int64_t tile) {
+__device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int64_t tile, char *smem) {
   const int64_t rows = b.rows[mi], cols = b.cols[mi];
   const int64_t kp = (cols + kQ4Pad - 1) / kQ4Pad * kQ4Pad, rp = (rows + kQ4Pad - 1) / kQ4Pad * kQ4Pad;
   const int64_t r16 = (rows + kQ4ScaleRow - 1) / kQ4ScaleRow * kQ4ScaleRow;
   const int64_t c16 = (cols + kQ4ScaleRow - 1) / kQ4ScaleRow * kQ4ScaleRow;
   uint8_t *const codes = b.codes[mi], *const codes_t = b.codes_t[mi];
-  const int64_t tc = ((codes ? kp : c16) + kTile - 1) / kTile;
+  const uint32_t tc = static_cast<uint32_t>(((codes ? kp : c16) + kTile - 1) / kTile);
+  const uint32_t ti = uniform(static_cast<uint32_t>(tile) / tc), tj = uniform(static_cast<uint32_t>(tile) - ti * tc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t r0 = tile / tc * kTile + wave * 32 + (lane >> 2 & 3) * 8;
-  const int64_t c0 = tile % tc * kTile + (lane >> 4) * 32 + (lane & 3) * 8;
-  float v[8][8];
-  uint8_t n[8][8] = {};
+  const int rl = wave * 32 + (lane >> 2 & 3) * 8, cl = (lane >> 4) * 32 + (lane & 3) * 8;
+  const int64_t r0 = static_cast<int64_t>(ti) * kTile + rl, c0 = static_cast<int64_t>(tj) * kTile + cl;
+  Eight<F32> x[8];
+  u32x2 n[8];
+  if (r0 + 8 <= rows && c0 + 8 <= cols) {
 #pragma unroll
-  for (int r = 0; r < 8; ++r)
+    for (int r = 0; r < 8; ++r) x[r].load(b.x[mi], (r0 + r) * cols + c0);
+    if constexpr (RANDOM)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool is = r0 + r < rows && c0 + k < cols;
-      const int64_t at = (r0 + r) * cols + c0 + k;
-      v[r][k] = is ? load_elem(b.x[mi], F32 ? kF32 : kBF16, at) : 0.f;
-      if constexpr (RANDOM) n[r][k] = is ? ((const g_u8 *)b.random[mi])[at] : 0;
-    }
-  if (codes) {
-    int bytes[8];
+      for (int r = 0; r < 8; ++r) n[r] = *(const g_u32x2_at1 *)(b.random[mi] + (r0 + r) * cols + c0);
+  } else {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      uint32_t a = 0;
+      const int64_t left = r0 + r < rows ? cols - c0 : 0;
+      x[r].load_some(b.x[mi], (r0 + r) * cols + c0, left);
+      n[r] = u32x2{0, 0};
+      if constexpr (RANDOM)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a = max(a, __float_as_uint(v[r][k]) & 0x7fffffffu);
-      bytes[r] = scale_byte(quad_max(a));
-      if (r0 + r < rows && c0 < kp) *(g_u32 *)(codes + (r0 + r) * (kp / 2) + c0 / 2) = codes8<RANDOM>(v[r], bytes[r], n[r]);
+        for (int k = 0; k < 8; ++k)
+          if (k < left) n[r][k / 4] |= static_cast<uint32_t>(((const g_u8 *)b.random[mi])[(r0 + r) * cols + c0 + k]) << (8 * (k % 4));
+    }
+  }
+  constexpr int W = F32 ? 8 : 4;
+  uint32_t col_max[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) col_max[k] = 0;
+  int bytes[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const uint32_t m = magnitude<F32>(x[r].w[k]);
+      a = larger<F32>(a, m);
+      col_max[k] = larger<F32>(col_max[k], m);
+    }
+    a = quad_max<F32>(a);
+    bytes[r] = scale_byte(F32 ? a : max(a << 16, a & 0xffff0000u));
+  }
+  if (codes) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = x[r].get(k);
+      const uint32_t w = codes8<RANDOM>(v, bytes[r], n[r]);
+      if (r0 + r < rows && c0 < kp) *(g_u32 *)(codes + (r0 + r) * (kp / 2) + c0 / 2) = w;
     }
     if ((lane & 3) == 0 && r0 < r16 && c0 < kp) *(g_u32x2 *)(b.scales[mi] + c0 / kQ4Block * r16 + r0) = pack8(bytes);
   }
-  if (codes_t) {
-    int bytes[8];
+  if (!codes_t) return;
+  lds_char *const lds = (lds_char *)smem;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float col[8];
-      uint8_t nc[8];
-      uint32_t a = 0;
+  for (int k = 0; k < W; ++k) col_max[k] = stride4_max<F32>(col_max[k]);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        col[r] = v[r][k];
-        nc[r] = n[r][k];
-        a = max(a, __float_as_uint(col[r]) & 0x7fffffffu);
-      }
-      bytes[k] = scale_byte(stride4_max(a));
-      if (c0 + k < cols && r0 < rp) *(g_u32 *)(codes_t + (c0 + k) * (rp / 2) + r0 / 2) = codes8<RANDOM>(col, bytes[k], nc);
+  for (int k = 0; k < 8; ++k) {
+    bytes[k] = scale_byte(F32 ? col_max[k % W] : k % 2 ? col_max[k / 2 % W] & 0xffff0000u : col_max[k / 2 % W] << 16);
+    float v[8];
+    u32x2 nc = {0, 0};
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      v[r] = x[r].get(k);
+      if constexpr (RANDOM) nc[r / 4] |= (n[r][k / 4] >> (8 * (k % 4)) & 0xff) << (8 * (r % 4));
     }
-    if ((lane & 12) == 0 && c0 < c16 && r0 < rp) *(g_u32x2 *)(b.scales_t[mi] + r0 / kQ4Block * c16 + c0) = pack8(bytes);
+    *(lds_u32 *)(lds + (cl + k) * kPitch + rl / 2) = codes8<RANDOM>(v, bytes[k], nc);
+  }
+  if ((lane & 12) == 0 && c0 < c16 && r0 < rp) *(g_u32x2 *)(b.scales_t[mi] + r0 / kQ4Block * c16 + c0) = pack8(bytes);
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = h * 64 + static_cast<int>(threadIdx.x >> 2), at = (threadIdx.x & 3) * 16;
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = *(const lds_u32 *)(lds + c * kPitch + at + 4 * k);
+    const int64_t col = static_cast<int64_t>(tj) * kTile + c, row = static_cast<int64_t>(ti) * kTile + 2 * at;
+    if (col < cols && row < rp) *(g_u32x4 *)(codes_t + col * (rp / 2) + row / 2) = w;
   }
 }
 
+template <bool F32, bool RANDOM>
 __global__ __launch_bounds__(kThreads) void q4_quantise_kernel(Q4Batch b) {
+  __shared__ __align__(16) char smem[kTile * kPitch];
   const int64_t w = blockIdx.x;
   const int32_t mi = find_range(b.n, w, [&](int32_t i) { return b.first_tile[i]; });
-  const int64_t tile = w - b.first_tile[mi];
-  if (b.random[mi]) {
-    if (b.dt[mi] == kF32)
-      quantise_tile<true, true>(b, mi, tile);
-    else
-      quantise_tile<false, true>(b, mi, tile);
-  } else {
-    if (b.dt[mi] == kF32)
-      quantise_tile<true, false>(b, mi, tile);
-    else
-      quantise_tile<false, false>(b, mi, tile);
-  }
+  quantise_tile<F32, RANDOM>(b, mi, w - b.first_tile[mi], smem);
+}
+
+template <bool F32, bool RANDOM>
+hipError_t launch_quantise(const Q4Batch &b, hipStream_t st) {
+  hipLaunchKernelGGL((q4_quantise_kernel<F32, RANDOM>), dim3(static_cast<uint32_t>(b.first_tile[b.n])), dim3(kThreads),
+                     0, st, b);
+  return hipGetLastError();
 }
 
 // Values of codes.  A work-group takes 256 columns (32 lanes of 8 codes) of 32
 // rows, so that the lines of the scale table it touches serve them all.  Every
 // code times its scale is a bf16 number, but for 4 * 2^126, which the largest
 // values round to and which becomes infinite.
+template <bool F32>
 __global__ __launch_bounds__(kThreads) void q4_dequantise_kernel(const uint8_t *__restrict__ codes,
                                                                  const uint8_t *__restrict__ scales, int64_t rows,
-                                                                 int64_t cols, void *__restrict__ out, int32_t dt) {
+                                                                 int64_t cols, void *__restrict__ out) {
   const int64_t kp = (cols + kQ4Pad - 1) / kQ4Pad * kQ4Pad;
   const int64_t r16 = (rows + kQ4ScaleRow - 1) / kQ4ScaleRow * kQ4ScaleRow;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 5);
   if (c >= cols) return;
+  uint32_t w[4];
+  int byte[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = min(r0 + 8 * i, rows - 1);
+    w[i] = *(const g_u32 *)(codes + r * (kp / 2) + c / 2);
+    byte[i] = ((const g_u8 *)scales)[c / kQ4Block * r16 + r];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + 8 * i;
     if (r >= rows) return;
-    const uint32_t w = *(const g_u32 *)(codes + r * (kp / 2) + c / 2);
-    const float s = scale_of(((const g_u8 *)scales)[c / kQ4Block * r16 + r]);
-    bf16x2 p[4];
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+    const float s = scale_of(byte[i]);
+    u32x4 p;
+    p.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 0));
+    p.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 1));
+    p.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 2));
+    p.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 3));
+    const int64_t at = r * cols + c;
+    if (!F32 && c + 8 <= cols) {
+      *(g_u32x4_at2 *)(static_cast<uint16_t *>(out) + at) = p;
+      continue;
+    }
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = static_cast<float>(p[k].x);
-      v[2 * k + 1] = static_cast<float>(p[k].y);
-    }
-    finish_run<8>(nullptr, out, dt, r * cols + c, cols - c, v);
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(k % 2 ? p[k / 2] & 0xffff0000u : p[k / 2] << 16);
+    finish_run<8>(nullptr, out, F32 ? kF32 : kBF16, at, cols - c, v);
   }
 }
 
@@ -204,14 +306,17 @@ int64_t q4_tiles(int64_t rows, int64_t cols, bool plain, bool transposed) {
 
 hipError_t launch_q4_quantize(const Q4Batch &b, hipStream_t st) {
   if (b.n == 0) return hipSuccess;
-  hipLaunchKernelGGL(q4_quantise_kernel, dim3(static_cast<uint32_t>(b.first_tile[b.n])), dim3(kThreads), 0, st, b);
-  return hipGetLastError();
+  if (b.random[0]) return b.dt == kF32 ? launch_quantise<true, true>(b, st) : launch_quantise<false, true>(b, st);
+  return b.dt == kF32 ? launch_quantise<true, false>(b, st) : launch_quantise<false, false>(b, st);
 }
 
 hipError_t launch_q4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                 int32_t dt, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>((rows + 31) / 32), static_cast<uint32_t>((cols + 255) / 256));
-  hipLaunchKernelGGL(q4_dequantise_kernel, grid, dim3(kThreads), 0, st, codes, scales, rows, cols, out, dt);
+  if (dt == kF32)
+    hipLaunchKernelGGL(q4_dequantise_kernel<true>, grid, dim3(kThreads), 0, st, codes, scales, rows, cols, out);
+  else
+    hipLaunchKernelGGL(q4_dequantise_kernel<false>, grid, dim3(kThreads), 0, st, codes, scales, rows, cols, out);
   return hipGetLastError();
 }
 

@@ -124,6 +124,17 @@ def test_weights(dtype, transposed):
             check_matrix(q, host(w), None, True, transposed)
 
 
+def test_weights_of_both_types():
+    """Types that change along the list, and with them the launches."""
+    print("weights of both types", flush=True)
+    rng = np.random.default_rng(6)
+    ws = [values(rng, n, k, F32 if i % 3 == 1 else BF16, 0.02) for i, (n, k) in enumerate(SIZES)]
+    got = nsd.q4_quantize_weights([w.cuda() for w in ws])
+    torch.cuda.synchronize()
+    for w, q in zip(ws, got):
+        check_matrix(q, host(w))
+
+
 def test_quantise_every_tie_and_range_end():
     """Every code, every tie between two codes and their fp32 neighbours, at the
     largest, the smallest and a middle scale; blocks of subnormals, zeros and the
