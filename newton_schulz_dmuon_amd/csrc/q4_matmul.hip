@@ -33,6 +33,162 @@ __device__ __forceinline__ void each(F f) {
   each(std::make_integer_sequence<int, N>{}, f);
 }
 
+// ---- few rows: the weight's bytes ----
+//
+// A work-group takes 16 NN outputs of up to 16 NT rows, its WAVES waves every
+// WAVES-th block of 256 codes; the waves' sums are added through LDS in wave order.
+// Each wave has a ring of stages of its own in LDS, and no barrier: it waits for
+// its own loads.  A block comes by LDS-bound loads of eight whole rows' 128 bytes,
+// the 16-byte chunks XORed with (row / 2) mod 8 against bank conflicts, its scales
+// by one more.  The weight's bytes are read once, the rows' from L2 once per 16 NN
+// outputs; of up to eight rows, XR = 8, eight are loaded.  Rows and outputs behind
+// the last are clamped for the loads and not stored.  Column r of row block j is
+// row r * NT + j, so that a lane's NT scale bytes are one LDS word.
+constexpr int stream_stage(int nt, int nn, int xr) { return nn * 2048 + nt * xr * 128 + (nn + nt) * 128; }
+// Blocks in flight a wave.
+constexpr int stream_ahead(int nt, int nn, int waves) { return waves == 8 || nt * nn > 2 ? 2 : 3; }
+
+template <int NT, int NN, int WAVES, int XR>
+__global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
+  constexpr int kAhead = stream_ahead(NT, NN, WAVES);
+  constexpr int kRows = NN * 2048, kScales = kRows + NT * XR * 128, kStage = stream_stage(NT, NN, XR);
+  constexpr int kLoads = 2 * NN + NT * XR / 8 + 1;  // vector loads a block
+  static_assert(XR == 16 || (XR == 8 && NT == 1));
+  __shared__ __attribute__((aligned(1024))) char smem[WAVES * kAhead * kStage];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * (16 * NT);
+  const int nkb = static_cast<int>(p.kp / kQ4Pad);
+  const uint32_t kpb = static_cast<uint32_t>(p.kp / 2);
+  const int64_t ra = (p.rows + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+  const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+  lds_char *const ring = (lds_char *)smem + wave * (kAhead * kStage);
+  // lane l of 1 KB load h of a block fills LDS row 8 h + l / 8, physical chunk l % 8
+  const uint8_t *const gb = p.b + n0 * kpb, *const ga = static_cast<const uint8_t *>(p.a) + t0 * kpb;
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(16 * NN - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(16 * NT - 1)));
+  uint32_t ob[NN][2], oa[NT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = 8 * h + (lane >> 3);
+    const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ ((row >> 1) & 7)) * 16;
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+      ob[i][h] = __umul24(static_cast<uint32_t>(min(i * 16 + row, lim_n)), kpb) + chunk;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      oa[j][h] = __umul24(static_cast<uint32_t>(min(row * NT + j, lim_t)), kpb) + chunk;
+  }
+  // the scales of a stage, 16 bytes a lane: [block][16 NN outputs], then [block]
+  // [16 NT rows]
+  const int sl = lane < 8 * NN ? lane : lane - 8 * NN;
+  const uint8_t *const scale0 =
+      lane < 8 * NN ? p.sb + sl / NN * rb + min(n0 + sl % NN * 16, rb - 16) : p.sa + sl / NT * ra + min(t0 + sl % NT * 16, ra - 16);
+  const int64_t scale_step = (lane < 8 * NN ? rb : ra) * (kQ4Pad / kQ4Block);
+  f32x4 acc[NN][NT];
+#pragma unroll
+  for (int i = 0; i < NN; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto load = [&](int u, int block) {
+    const int kb = min(block, nkb - 1);
+    lds_char *const st = ring + u * kStage;
+    auto piece = [&](const uint8_t *src, int at) {
+      __builtin_amdgcn_global_load_lds((const void *)src, (__attribute__((address_space(3))) void *)(st + at), 16, 0, 0);
+    };
+    const uint8_t *const bb = gb + static_cast<int64_t>(kb) * 128, *const ba = ga + static_cast<int64_t>(kb) * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < NN; ++i) piece(bb + ob[i][h], i * 2048 + h * 1024);
+      if (8 * h < XR)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) piece(ba + oa[j][h], kRows + j * (XR * 128) + h * 1024);
+    }
+    if (lane < 8 * (NN + NT)) piece(scale0 + kb * scale_step, kScales);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // a lane's codes of row r16 of a block: chunks g4 and g4 + 4
+  auto at = [&](int row) { return static_cast<uint32_t>(row * 128 + ((g4 ^ (row >> 1)) & 7) * 16); };
+  const uint32_t at_b = at(r16), at_a = at(r16 & (XR - 1));
+  u32x4 fb[NN][2], fa[NT][2];
+  uint32_t sb[NN][2], sa[2];
+  auto read = [&](int u) {
+    const lds_char *const st = ring + u * kStage;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < NN; ++i) {
+        fb[i][s] = *(const lds_u32x4 *)(st + i * 2048 + (s ? at_b ^ 64 : at_b));
+        sb[i][s] = *(const lds_u8 *)(st + kScales + (4 * s + g4) * (16 * NN) + i * 16 + r16);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fa[j][s] = *(const lds_u32x4 *)(st + kRows + j * (XR * 128) + (s ? at_a ^ 64 : at_a));
+      const lds_char *const ws = st + kScales + NN * 128 + (4 * s + g4) * (16 * NT) + r16 * NT;
+      if constexpr (NT == 4)
+        sa[s] = *(const lds_u32 *)ws;
+      else if constexpr (NT == 2)
+        sa[s] = *(const lds_u16 *)ws;
+      else
+        sa[s] = *(const lds_u8 *)ws;
+    }
+    // all are in registers before the stage is loaded again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      each<NN>([&](auto i) {
+        each<NT>([&](auto j) { acc[i][j] = q4_product<0, j>(fb[i][s], sb[i][s], fa[j][s], sa[s], acc[i][j]); });
+      });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, wave + u * WAVES);
+  // each stage takes the block kAhead further on as soon as its codes have been
+  // read; the last kAhead blocks load nothing more
+  int k0 = wave;
+  for (; k0 + WAVES * kAhead < nkb; k0 += WAVES * kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+      read(u);
+      load(u, k0 + (kAhead + u) * WAVES);
+      multiply();
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (k0 + u * WAVES < nkb) {
+      read(u);
+      multiply();
+    }
+  // the waves' sums, each in its own part of the ring
+  auto part = [&](int w, int b) { return (lds_f32x4 *)((lds_char *)smem + w * (kAhead * kStage) + b * 1024 + lane * 16); };
+  static_assert(NN * NT * 1024 <= kAhead * kStage);
+#pragma unroll
+  for (int i = 0; i < NN; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *part(wave, i * NT + j) = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < (NN * NT + WAVES - 1) / WAVES; ++q) {
+    const int b = q * WAVES + wave;
+    if (b >= NN * NT) return;
+    f32x4 sum = *part(0, b);
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) sum += *part(w, b);
+    const int64_t t = t0 + r16 * NT + b % NT, n = n0 + b / NT * 16 + 4 * g4;
+    if (t >= p.rows) continue;
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    finish_run<4>(p.base, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
+  }
+}
+
 // ---- tiles: many rows ----
 //
 // One work-group of 8 waves (2 x 4) computes TA outputs of the weight by TB
@@ -217,9 +373,45 @@ __global__ __launch_bounds__(256) void q4_empty_kernel(Q4Product p) {
 constexpr std::initializer_list<TileCost> kCosts = {
     {256, 256, 1, 1.03f, 1.5f}, {128, 256, 1, 0.8f, 0.97f}, {128, 128, 2, 0.6f, 1.06f}};
 
-TileSplit plan_of(int64_t rows, int64_t outs, int64_t kp) {
-  if (rows == 0 || kp == 0) return TileSplit{};
-  return choose_split(outs, rows, kp / kQ4Pad, kCosts);
+// How a product runs: streamed (row blocks, output blocks and waves of a
+// work-group) or in tiles.
+struct Plan {
+  int nt, nn, waves;  // nt = 0: tiles
+  TileSplit split;
+};
+
+// The streaming kernel's time in microseconds: a work-group takes in its weight's
+// and rows' codes at 53 GB/s, 256 of them at a time, while the weight comes from
+// memory at 4.9 TB/s; a quarter of the shorter of the two does not hide.
+float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
+  const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
+  const float bytes = static_cast<float>((16 * nn + (rows <= 8 ? 8 : std::min<int64_t>(16 * nt, rows))) * kp) * 0.53f;
+  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
+  const float memory = static_cast<float>(outs * kp) * 0.53f / 4.9e6f;
+  return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
+}
+// Rows up to which it is considered.
+constexpr int64_t kStreamRows = 1024;
+
+Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
+  Plan pl{};
+  if (rows == 0 || kp == 0) return pl;
+  float us;
+  pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
+  if (rows > kStreamRows) return pl;
+  for (const int nt : {1, 2, 4})
+    for (const int nn : {1, 2}) {
+      const float s = stream_us(rows, outs, kp, nt, nn);
+      if (s >= us) continue;
+      us = s;
+      pl.nt = nt;
+      pl.nn = nn;
+    }
+  if (pl.nt) {
+    pl.waves = pl.nt * pl.nn == 1 && kp >= 32 * kQ4Pad ? 8 : 4;
+    pl.split = TileSplit{};
+  }
+  return pl;
 }
 
 template <int TA, int TB>
@@ -228,9 +420,32 @@ hipError_t launch_tiles(const Q4Product &p, const TileSplit &sp, hipStream_t st)
   return hipGetLastError();
 }
 
+template <int NT, int NN, int WAVES, int XR>
+hipError_t launch_stream(const Q4Product &p, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN) * ((p.rows + 16 * NT - 1) / (16 * NT))));
+  hipLaunchKernelGGL((q4_stream_kernel<NT, NN, WAVES, XR>), grid, dim3(WAVES * 64), 0, st, p);
+  return hipGetLastError();
+}
+
+template <int NT, int NN>
+hipError_t launch_stream(const Q4Product &p, int waves, hipStream_t st) {
+  if constexpr (NT * NN <= 2)
+    if (waves == 8) {
+      if (NT == 1 && p.rows <= 8) return launch_stream<NT, NN, 8, NT == 1 ? 8 : 16>(p, st);
+      return launch_stream<NT, NN, 8, 16>(p, st);
+    }
+  if (NT == 1 && p.rows <= 8) return launch_stream<NT, NN, 4, NT == 1 ? 8 : 16>(p, st);
+  return launch_stream<NT, NN, 4, 16>(p, st);
+}
+
+template <int NT>
+hipError_t launch_stream(const Q4Product &p, const Plan &pl, hipStream_t st) {
+  return pl.nn == 2 ? launch_stream<NT, 2>(p, pl.waves, st) : launch_stream<NT, 1>(p, pl.waves, st);
+}
+
 }  // namespace
 
-size_t q4_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) { return plan_of(rows, outs, kp).ws_bytes(); }
+size_t q4_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) { return plan_of(rows, outs, kp).split.ws_bytes(); }
 
 hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
   if (p.kp == 0) {
@@ -238,7 +453,11 @@ hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
     hipLaunchKernelGGL(q4_empty_kernel, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, st, p);
     return hipGetLastError();
   }
-  const TileSplit sp = plan_of(p.rows, p.outs, p.kp);
+  const Plan pl = plan_of(p.rows, p.outs, p.kp);
+  if (pl.nt == 1) return launch_stream<1>(p, pl, st);
+  if (pl.nt == 2) return launch_stream<2>(p, pl, st);
+  if (pl.nt == 4) return launch_stream<4>(p, pl, st);
+  const TileSplit &sp = pl.split;
   const hipError_t e = sp.ta == 256   ? launch_tiles<256, 256>(p, sp, st)
                        : sp.tb == 256 ? launch_tiles<128, 256>(p, sp, st)
                                       : launch_tiles<128, 128>(p, sp, st);

@@ -171,7 +171,10 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int64_t left = r0 + r < rows ? cols - c0 : 0;
-      x[r].load_some(b.x[mi], (r0 + r) * cols + c0, left);
+      if (left >= 8)
+        x[r].load(b.x[mi], (r0 + r) * cols + c0);
+      else
+        x[r].load_some(b.x[mi], (r0 + r) * cols + c0, left);
       n[r] = u32x2{0, 0};
       if constexpr (RANDOM)
 #pragma unroll
