@@ -400,7 +400,8 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
   pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
   if (rows > kStreamRows) return pl;
   for (const int nt : {1, 2, 4})
-    for (const int nn : {1, 2}) {
+    for (const int nn : {1, 2, 4}) {
+      if (nn == 4 && nt != 4) continue;
       const float s = stream_us(rows, outs, kp, nt, nn);
       if (s >= us) continue;
       us = s;
@@ -408,7 +409,7 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
       pl.nn = nn;
     }
   if (pl.nt) {
-    pl.waves = pl.nt * pl.nn == 1 && kp >= 32 * kQ4Pad ? 8 : 4;
+    pl.waves = pl.nt * pl.nn == 1 && kp >= 16 * kQ4Pad ? 8 : 4;
     pl.split = TileSplit{};
   }
   return pl;
@@ -440,6 +441,8 @@ hipError_t launch_stream(const Q4Product &p, int waves, hipStream_t st) {
 
 template <int NT>
 hipError_t launch_stream(const Q4Product &p, const Plan &pl, hipStream_t st) {
+  if constexpr (NT == 4)
+    if (pl.nn == 4) return launch_stream<4, 4>(p, pl.waves, st);
   return pl.nn == 2 ? launch_stream<NT, 2>(p, pl.waves, st) : launch_stream<NT, 1>(p, pl.waves, st);
 }
 

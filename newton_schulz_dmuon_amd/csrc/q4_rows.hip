@@ -29,8 +29,8 @@ struct Rows {
 
 // ---- few rows: the weight's bytes ----
 //
-// A work-group takes 16 NN outputs of up to 16 NT rows, its WAVES waves every
-// WAVES-th block of 256 codes; the waves' sums are added through LDS in wave order.
+// A work-group takes 16 NN outputs of up to 16 rows, its four waves every fourth
+// block of 256 codes; the waves' sums are added through LDS in wave order.
 // Each wave has a ring of stages of its own in LDS, and no barrier: it waits for
 // its own loads.  A block comes by LDS-bound loads: eight outputs' 128 bytes of
 // codes each, the 16-byte chunks XORed with (output / 2) mod 8; two rows' 512 bytes
@@ -41,24 +41,22 @@ struct Rows {
 //
 // A lane's 32 codes of a chunk (one block of the format) are multiplied eight an
 // instruction.
-constexpr int stream_stage(int nt, int nn, int xr) { return nn * (2048 + 128) + nt * xr * 512; }
+constexpr int kStreamWaves = 4;
+constexpr int stream_stage(int nn, int xr) { return nn * (2048 + 128) + xr * 512; }
 // Blocks in flight a wave.
-constexpr int stream_ahead(int nt, int nn, int waves, int xr) {
-  return 3 * waves * stream_stage(nt, nn, xr) <= 80 * 1024 ? 3 : 2;
-}
+constexpr int stream_ahead(int nn, int xr) { return 3 * kStreamWaves * stream_stage(nn, xr) <= 80 * 1024 ? 3 : 2; }
 
-template <int NT, int NN, int WAVES, int XR>
-__global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p, Rows x) {
-  constexpr int kAhead = stream_ahead(NT, NN, WAVES, XR);
-  constexpr int kScales = NN * 2048, kRows = kScales + NN * 128, kStage = stream_stage(NT, NN, XR);
-  constexpr int kLoads = 2 * NN + NT * XR / 2 + 1;  // vector loads a block
-  static_assert(XR == 16 || (XR >= 2 && NT == 1));
-  __shared__ __attribute__((aligned(1024))) char smem[WAVES * kAhead * kStage];
+template <int NN, int XR>
+__global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Product p, Rows x) {
+  constexpr int kAhead = stream_ahead(NN, XR);
+  constexpr int kScales = NN * 2048, kRows = kScales + NN * 128, kStage = stream_stage(NN, XR);
+  constexpr int kLoads = 2 * NN + XR / 2 + 1;  // vector loads a block
+  __shared__ __attribute__((aligned(1024))) char smem[kStreamWaves * kAhead * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * (16 * NT);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * 16;
   const int nkb = static_cast<int>(p.kp / kQ4Pad);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
@@ -67,8 +65,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p,
   // l % 8; of the rows LDS row 2 h + l / 32, physical chunk l % 32
   const uint8_t *const gb = p.b + n0 * kpb, *const ga = x.x + t0 * ldb;
   const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(16 * NN - 1)));
-  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(16 * NT - 1)));
-  uint32_t ob[NN][2], oa[NT * XR / 2];
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(15)));
+  uint32_t ob[NN][2], oa[XR / 2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int row = 8 * h + (lane >> 3);
@@ -78,17 +76,15 @@ __global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p,
       ob[i][h] = __umul24(static_cast<uint32_t>(min(i * 16 + row, lim_n)), kpb) + chunk;
   }
 #pragma unroll
-  for (int h = 0; h < NT * XR / 2; ++h) {
+  for (int h = 0; h < XR / 2; ++h) {
     const int row = 2 * h + (lane >> 5);
     oa[h] = __umul24(static_cast<uint32_t>(min(row, lim_t)), ldb) + static_cast<uint32_t>((lane & 31) ^ (row & 15)) * 16;
   }
   // the scales of a stage, 16 bytes a lane: [block][16 NN outputs]
   const uint8_t *const scale0 = p.sb + lane / NN % 8 * rb + min(n0 + lane % NN * 16, rb - 16);
-  f32x4 acc[NN][NT];
+  f32x4 acc[NN];
 #pragma unroll
-  for (int i = 0; i < NN; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NN; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto load = [&](int u, int block) {
     const int kb = min(block, nkb - 1);
     lds_char *const st = ring + u * kStage;
@@ -101,13 +97,13 @@ __global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p,
 #pragma unroll
       for (int h = 0; h < 2; ++h) piece(bb + ob[i][h], i * 2048 + h * 1024);
 #pragma unroll
-    for (int h = 0; h < NT * XR / 2; ++h) piece(ba + oa[h], kRows + h * 1024);
+    for (int h = 0; h < XR / 2; ++h) piece(ba + oa[h], kRows + h * 1024);
     if (lane < 8 * NN) piece(scale0 + static_cast<int64_t>(kb) * (kQ4Pad / kQ4Block) * rb, kScales);
     __builtin_amdgcn_sched_barrier(0);
   };
   const uint32_t at_b = static_cast<uint32_t>(r16 * 128 + ((g4 ^ (r16 >> 1)) & 7) * 16);
   const int xrow = r16 & (XR - 1);
-  u32x4 fb[NN][2], fa[NT][8];
+  u32x4 fb[NN][2], fa[8];
   float s[NN][2];
   auto read = [&](int u) {
     const lds_char *const st = ring + u * kStage;
@@ -119,10 +115,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p,
         s[i][h] = q4_half_scale(*(const lds_u8 *)(st + kScales + (4 * h + g4) * (16 * NN) + i * 16 + r16));
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-          fa[j][4 * h + d] = *(const lds_u32x4 *)(st + kRows + j * (XR * 512) + xrow * 512 + (((4 * h + g4) * 4 + d) ^ xrow) * 16);
+      for (int d = 0; d < 4; ++d)
+        fa[4 * h + d] = *(const lds_u32x4 *)(st + kRows + xrow * 512 + (((4 * h + g4) * 4 + d) ^ xrow) * 16);
     }
     // all are in registers before the stage is loaded again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -134,55 +128,46 @@ __global__ __launch_bounds__(WAVES * 64) void q4_rows_stream_kernel(Q4Product p,
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
-        for (int i = 0; i < NN; ++i) {
-          const bf16x8 xb = q4_expand8(fb[i][h][d], s[i][h]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, fa[j][4 * h + d]), acc[i][j], 0, 0, 0);
-        }
+        for (int i = 0; i < NN; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q4_expand8(fb[i][h][d], s[i][h]),
+                                                           __builtin_bit_cast(bf16x8, fa[4 * h + d]), acc[i], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, wave + u * WAVES);
+  for (int u = 0; u < kAhead; ++u) load(u, wave + u * kStreamWaves);
   // each stage takes the block kAhead further on as soon as it has been read; the
   // last kAhead blocks load nothing more
   int k0 = wave;
-  for (; k0 + WAVES * kAhead < nkb; k0 += WAVES * kAhead) {
+  for (; k0 + kStreamWaves * kAhead < nkb; k0 += kStreamWaves * kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kLoads) : "memory");
       read(u);
-      load(u, k0 + (kAhead + u) * WAVES);
+      load(u, k0 + (kAhead + u) * kStreamWaves);
       multiply();
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (k0 + u * WAVES < nkb) {
+    if (k0 + u * kStreamWaves < nkb) {
       read(u);
       multiply();
     }
   // the waves' sums, each in its own part of the ring
   auto part = [&](int w, int b) { return (lds_f32x4 *)((lds_char *)smem + w * (kAhead * kStage) + b * 1024 + lane * 16); };
-  static_assert(NN * NT * 1024 <= kAhead * kStage);
+  static_assert(NN * 1024 <= kAhead * kStage && NN <= kStreamWaves);
 #pragma unroll
-  for (int i = 0; i < NN; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) *part(wave, i * NT + j) = acc[i][j];
+  for (int i = 0; i < NN; ++i) *part(wave, i) = acc[i];
   __syncthreads();
+  if (wave >= NN) return;
+  f32x4 sum = *part(0, wave);
 #pragma unroll
-  for (int q = 0; q < (NN * NT + WAVES - 1) / WAVES; ++q) {
-    const int b = q * WAVES + wave;
-    if (b >= NN * NT) return;
-    f32x4 sum = *part(0, b);
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += *part(w, b);
-    const int64_t t = t0 + b % NT * 16 + r16, n = n0 + b / NT * 16 + 4 * g4;
-    if (t >= p.rows) continue;
-    float v[4] = {2.f * sum[0], 2.f * sum[1], 2.f * sum[2], 2.f * sum[3]};
-    finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
-  }
+  for (int w = 1; w < kStreamWaves; ++w) sum += *part(w, wave);
+  const int64_t t = t0 + r16, n = n0 + wave * 16 + 4 * g4;
+  if (t >= p.rows) return;
+  float v[4] = {2.f * sum[0], 2.f * sum[1], 2.f * sum[2], 2.f * sum[3]};
+  finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
 }
 
 // ---- tiles: many rows ----
@@ -357,28 +342,24 @@ void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
 constexpr std::initializer_list<TileCost> kCosts = {
     {256, 256, 1, 4.5f, 5.8f}, {128, 256, 1, 2.8f, 3.4f}, {128, 128, 2, 1.9f, 3.8f}};
 
-// How a product runs: streamed (row blocks, output blocks and waves of a
-// work-group) or in tiles; its rows' distance; and the bytes of its workspace's two
+// How a product runs: streamed (output blocks of a work-group) or in tiles; its rows' distance; and the bytes of its workspace's two
 // parts, the padded rows and the pieces' results.
 struct Plan {
-  int nt, nn, waves;  // nt = 0: tiles
+  int nn;  // 0: tiles
   TileSplit split;
   int64_t ld;
   size_t pad_bytes, piece_bytes;
 };
 
 // Rows that a streaming work-group loads.
-int64_t stream_rows(int64_t rows, int nt) {
-  if (nt > 1 || rows > 8) return 16 * nt;
-  return rows > 4 ? 8 : rows > 2 ? 4 : 2;
-}
+int64_t stream_rows(int64_t rows) { return rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : 2; }
 
 // The streaming kernel's time in microseconds: a work-group takes in its weight's
 // codes and its rows at 53 GB/s, 256 of them at a time, while the weight comes from
 // memory at 4.9 TB/s; a quarter of the shorter of the two does not hide.
-float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
-  const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
-  const float bytes = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(stream_rows(rows, nt)));
+float stream_us(int64_t rows, int64_t outs, int64_t kp, int nn) {
+  const int64_t groups = (rows + 15) / 16 * ((outs + 16 * nn - 1) / (16 * nn));
+  const float bytes = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(stream_rows(rows)));
   const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
   const float memory = static_cast<float>(outs * kp) * 0.53f / 4.9e6f;
   return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
@@ -393,22 +374,16 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
   float us;
   pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
   if (rows <= kStreamRows) {
-    for (const int nt : {1, 2})
-      for (const int nn : {1, 2}) {
-        if (nt == 2 && nn == 2) continue;
-        const float s = stream_us(rows, outs, kp, nt, nn);
-        if (s >= us) continue;
-        us = s;
-        pl.nt = nt;
-        pl.nn = nn;
-      }
-    if (pl.nt) {
-      pl.waves = stream_rows(rows, pl.nt) <= 8 && pl.nn == 1 && kp >= 32 * kQ4Pad ? 8 : 4;
-      pl.split = TileSplit{};
+    for (const int nn : {1, 2, 4}) {
+      const float s = stream_us(rows, outs, kp, nn);
+      if (s >= us) continue;
+      us = s;
+      pl.nn = nn;
     }
+    if (pl.nn) pl.split = TileSplit{};
   }
   // PLAN_HOOK
-  const int64_t step = pl.nt ? kQ4Pad : kStep;
+  const int64_t step = pl.nn ? kQ4Pad : kStep;
   pl.ld = (inner + step - 1) / step * step;
   if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
   pl.piece_bytes = pl.split.ws_bytes();
@@ -422,20 +397,20 @@ hipError_t launch_tiles(const Q4Product &p, const Rows &x, const TileSplit &sp, 
   return hipGetLastError();
 }
 
-template <int NT, int NN, int WAVES, int XR>
+template <int NN, int XR>
 hipError_t launch_stream(const Q4Product &p, const Rows &x, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN) * ((p.rows + 16 * NT - 1) / (16 * NT))));
-  hipLaunchKernelGGL((q4_rows_stream_kernel<NT, NN, WAVES, XR>), grid, dim3(WAVES * 64), 0, st, p, x);
+  const dim3 grid(static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN) * ((p.rows + 15) / 16)));
+  hipLaunchKernelGGL((q4_rows_stream_kernel<NN, XR>), grid, dim3(kStreamWaves * 64), 0, st, p, x);
   return hipGetLastError();
 }
 
-template <int NN, int WAVES>
+template <int NN>
 hipError_t launch_stream(const Q4Product &p, const Rows &x, hipStream_t st) {
-  switch (stream_rows(p.rows, 1)) {
-    case 2: return launch_stream<1, NN, WAVES, 2>(p, x, st);
-    case 4: return launch_stream<1, NN, WAVES, 4>(p, x, st);
-    case 8: return launch_stream<1, NN, WAVES, 8>(p, x, st);
-    default: return launch_stream<1, NN, 4, 16>(p, x, st);
+  switch (stream_rows(p.rows)) {
+    case 2: return launch_stream<NN, 2>(p, x, st);
+    case 4: return launch_stream<NN, 4>(p, x, st);
+    case 8: return launch_stream<NN, 8>(p, x, st);
+    default: return launch_stream<NN, 16>(p, x, st);
   }
 }
 
@@ -456,9 +431,9 @@ hipError_t launch_q4_rows(const Q4Product &args, hipStream_t st) {
     x.x = static_cast<const uint8_t *>(p.ws);
     p.ws = static_cast<char *>(p.ws) + pl.pad_bytes;
   }
-  if (pl.nt == 2) return launch_stream<2, 1, 4, 16>(p, x, st);
-  if (pl.nt == 1 && pl.nn == 2) return pl.waves == 8 ? launch_stream<2, 8>(p, x, st) : launch_stream<2, 4>(p, x, st);
-  if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, x, st) : launch_stream<1, 4>(p, x, st);
+  if (pl.nn == 1) return launch_stream<1>(p, x, st);
+  if (pl.nn == 2) return launch_stream<2>(p, x, st);
+  if (pl.nn == 4) return launch_stream<4>(p, x, st);
   const TileSplit &sp = pl.split;
   const hipError_t e = sp.ta == 256   ? launch_tiles<256, 256>(p, x, sp, st)
                        : sp.tb == 256 ? launch_tiles<128, 256>(p, x, sp, st)
