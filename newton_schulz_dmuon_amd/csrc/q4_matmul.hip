@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void q4_empty_kernel(Q4Product p) {
 }
 
 constexpr std::initializer_list<TileCost> kCosts = {
-    {256, 256, 1, 1.03f, 1.5f}, {128, 256, 1, 0.8f, 0.97f}, {128, 128, 2, 0.6f, 1.06f}};
+    {256, 256, 1, 1.2f, 1.85f}, {128, 256, 1, 0.85f, 1.04f}, {128, 128, 2, 0.7f, 1.15f}};
 
 // How a product runs: streamed (row blocks, output blocks and waves of a
 // work-group) or in tiles.
@@ -385,7 +385,7 @@ struct Plan {
 // memory at 4.9 TB/s; a quarter of the shorter of the two does not hide.
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
-  const float bytes = static_cast<float>((16 * nn + (rows <= 8 ? 8 : std::min<int64_t>(16 * nt, rows))) * kp) * 0.53f;
+  const float bytes = static_cast<float>((16 * nn + (rows <= 8 && nt == 1 ? 8 : 16 * nt)) * kp) * 0.53f;
   const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
   const float memory = static_cast<float>(outs * kp) * 0.53f / 4.9e6f;
   return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
@@ -398,20 +398,22 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
   if (rows == 0 || kp == 0) return pl;
   float us;
   pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
-  if (rows > kStreamRows) return pl;
-  for (const int nt : {1, 2, 4})
-    for (const int nn : {1, 2, 4}) {
-      if (nn == 4 && nt != 4) continue;
-      const float s = stream_us(rows, outs, kp, nt, nn);
-      if (s >= us) continue;
-      us = s;
-      pl.nt = nt;
-      pl.nn = nn;
+  if (rows <= kStreamRows) {
+    for (const int nt : {1, 2, 4})
+      for (const int nn : {1, 2, 4}) {
+        if (nn == 4 && nt != 4) continue;
+        const float s = stream_us(rows, outs, kp, nt, nn);
+        if (s >= us) continue;
+        us = s;
+        pl.nt = nt;
+        pl.nn = nn;
+      }
+    if (pl.nt) {
+      pl.waves = pl.nt * pl.nn == 1 && kp >= 16 * kQ4Pad ? 8 : 4;
+      pl.split = TileSplit{};
     }
-  if (pl.nt) {
-    pl.waves = pl.nt * pl.nn == 1 && kp >= 16 * kQ4Pad ? 8 : 4;
-    pl.split = TileSplit{};
   }
+  // PLAN_HOOK
   return pl;
 }
 

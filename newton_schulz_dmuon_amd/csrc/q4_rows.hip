@@ -340,7 +340,7 @@ void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
 }
 
 constexpr std::initializer_list<TileCost> kCosts = {
-    {256, 256, 1, 4.5f, 5.8f}, {128, 256, 1, 2.8f, 3.4f}, {128, 128, 2, 1.9f, 3.8f}};
+    {256, 256, 1, 4.7f, 6.15f}, {128, 256, 1, 3.2f, 3.5f}, {128, 128, 2, 2.6f, 4.03f}};
 
 // How a product runs: streamed (output blocks of a work-group) or in tiles; its rows' distance; and the bytes of its workspace's two
 // parts, the padded rows and the pieces' results.
