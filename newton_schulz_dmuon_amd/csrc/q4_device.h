@@ -21,10 +21,9 @@ __device__ __forceinline__ f32x4 q4_product(const u32x4 &b, uint32_t sb, const u
                                                           static_cast<int>(sb), IA, static_cast<int>(sa));
 }
 
-// 2^(byte - 128) as fp32, half of a scale byte's scale; NaN for kQ4Nan.
-__device__ __forceinline__ float q4_half_scale(uint32_t byte) {
-  return __uint_as_float(byte == kQ4Nan ? 0x7fc00000u : (byte - 1) << 23);
-}
+// 2^(byte - 128) as fp32, half of a scale byte's scale; infinity for kQ4Nan, with
+// which every conversion from a code gives NaN.
+__device__ __forceinline__ float q4_half_scale(uint32_t byte) { return __uint_as_float(byte << 23) * 0.5f; }
 
 // Eight codes (a word) times a power of two as bf16, exactly.
 __device__ __forceinline__ bf16x8 q4_expand8(uint32_t w, float s) {
@@ -33,6 +32,31 @@ __device__ __forceinline__ bf16x8 q4_expand8(uint32_t w, float s) {
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Adds the sums of two waves that share a tile and split k: wave `half` 0 keeps the
+// rows' blocks j < FN / 2, half 1 the others, and each gets the other's part of its
+// own through LDS (slot: 1 KB times FM FN / 2 of each of the pair's waves).  The
+// first half's sum is the first operand.  `mine` and `other` are the two waves'
+// slots; every wave of the work-group takes part.
+template <int FM, int FN>
+__device__ __forceinline__ void exchange_halves(f32x4 (&acc)[FM][FN], int half, lds_char *mine, lds_char *other) {
+  const int at = (threadIdx.x & 63) * 16;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN / 2; ++j) {
+      const f32x4 give = half == 0 ? acc[i][j + FN / 2] : acc[i][j];
+      *(lds_f32x4 *)(mine + (i * (FN / 2) + j) * 1024 + at) = give;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN / 2; ++j) {
+      const f32x4 got = *(const lds_f32x4 *)(other + (i * (FN / 2) + j) * 1024 + at);
+      acc[i][j] = half == 0 ? acc[i][j] + got : got + acc[i][j + FN / 2];
+    }
 }
 
 }  // namespace dmuon

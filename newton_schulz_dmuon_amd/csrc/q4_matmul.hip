@@ -191,8 +191,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
 
 // ---- tiles: many rows ----
 //
-// One work-group of 8 waves (2 x 4) computes TA outputs of the weight by TB
-// rows; each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 256 codes (128 bytes,
+// One work-group of 8 waves (2 x 4) computes TA (128 or 256) outputs of the weight
+// by 256 rows, TB below; each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 256 codes (128 bytes,
 // 8 blocks of the format) per step.  Both operand tiles go from global memory into
 // LDS by LDS-bound loads (16 bytes a lane, 128-byte rows, the 16-byte chunk, a
 // block of the format, XORed with (row / 2) mod 8, which keeps the fragment reads
@@ -207,14 +207,14 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
 // blocks) are consecutive and its quarter-wave neighbours' follow, and block j,
 // column r of the rows' operand holds row r * FN + j.  A lane's FM or FN scale bytes
 // of a block of k are then consecutive bytes of the scale table's row.
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 512, kTileRows = 256;
 constexpr int kRowBytes = 128;
 constexpr int kStepBlocks = kQ4Pad / kQ4Block;
 
-template <int TA, int TB>
+template <int TA>
 __device__ __forceinline__ void q4_tile(lds_char *const lds, const Q4Product &p, int64_t n0, int64_t t0, int kbeg,
-                                        int kend, f32x4 (&acc)[TA / 32][TB / 64]) {
-  constexpr int FM = TA / 32, FN = TB / 64;
+                                        int kend, f32x4 (&acc)[TA / 32][kTileRows / 64]) {
+  constexpr int TB = kTileRows, FM = TA / 32, FN = TB / 64;
   // a stage: the weight's tile, the rows', the weight's scales (each half's [block]
   // [output]), the rows' ([block][row])
   constexpr int kWeight = TA * kRowBytes, kScaleA = kWeight + TB * kRowBytes, kScaleB = kScaleA + TA * kStepBlocks;
@@ -307,10 +307,7 @@ __device__ __forceinline__ void q4_tile(lds_char *const lds, const Q4Product &p,
       } else {
         sb[0][s] = *(const lds_u32 *)(st + at_b + s * (4 * TA / 2));
       }
-      if constexpr (FN == 4)
-        sa[s] = *(const lds_u32 *)(st + at_a + s * (4 * TB));
-      else
-        sa[s] = *(const lds_u16 *)(st + at_a + s * (4 * TB));
+      sa[s] = *(const lds_u32 *)(st + at_a + s * (4 * TB));
 #pragma unroll
       for (int i = 0; i < FM; ++i) fb[i][s] = read(opb, i, s);
 #pragma unroll
@@ -333,15 +330,15 @@ __device__ __forceinline__ void q4_tile(lds_char *const lds, const Q4Product &p,
   if (wm == 0) barrier();
 }
 
-template <int TA, int TB>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TB == 256 ? 2 : 4)))
+template <int TA>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void q4_tile_kernel(Q4Product p, TileSplit sp) {
-  constexpr int FM = TA / 32, FN = TB / 64;
+  constexpr int TB = kTileRows, FM = TA / 32, FN = TB / 64;
   __shared__ __attribute__((aligned(1024))) char smem[2 * (TA + TB) * (kRowBytes + kStepBlocks)];
   const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
   const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
   f32x4 acc[FM][FN];
-  q4_tile<TA, TB>((lds_char *)smem, p, n0, t0, w.begin, w.end, acc);
+  q4_tile<TA>((lds_char *)smem, p, n0, t0, w.begin, w.end, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
@@ -361,6 +358,150 @@ void q4_tile_kernel(Q4Product p, TileSplit sp) {
   }
 }
 
+// ---- small tiles: a deep ring ----
+//
+// 128 outputs by TB (64 or 128) rows, one work-group a CU, for launches of few tiles,
+// which the latency of a step bounds.  Eight waves: 2 x 2 parts of 64 x TB / 2, and
+// two halves of a step's 256 codes, whose sums are added at the end (one wave for
+// all codes and half the part would read half as much again from LDS).  A ring of
+// four stages: a step waits for its own stage, loaded three steps ago, meets the
+// other waves once, loads the stage that all of them have left and multiplies.  The
+// two waves of a SIMD hide each other's reads.
+//
+// A lane's four rows of a weight block (q = 4 g4 + v) and FM blocks are consecutive
+// outputs: block i, row q holds output q * FM + i of the wave's part, block j,
+// column r of the rows' operand row r * FN + j.
+constexpr int kMidThreads = 512;
+
+template <int TB>
+__global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void q4_mid_kernel(Q4Product p, TileSplit sp) {
+  constexpr int TA = 128, FM = TA / 32, FN = TB / 32, kMidStages = TB == 128 ? 4 : 6;
+  constexpr int kRows = TA * kRowBytes, kScaleB = kRows + TB * kRowBytes, kScaleA = kScaleB + TA * kStepBlocks;
+  constexpr int kStage = kScaleA + TB * kStepBlocks;
+  constexpr int kLoads = (TA + TB) / 64 + 1;  // vector loads a wave and stage
+  constexpr int kScaleLanes = (TA + TB) * kStepBlocks / 16 / 8;  // 16 bytes each
+  __shared__ __attribute__((aligned(1024))) char smem[kMidStages * kStage];
+  lds_char *const lds = (lds_char *)smem;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2, wm = wave >> 1 & 1, wn = wave & 1, r16 = lane & 15, g4 = lane >> 4;
+  const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
+  const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
+  const uint32_t kpb = static_cast<uint32_t>(p.kp / 2);
+  const int64_t ra = (p.rows + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+  const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TA - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TB - 1)));
+  // load j of a wave fills LDS rows 8 (wave + 8 j) ..: lane l row l / 8, physical
+  // chunk l % 8
+  uint32_t ob[TA / 64], oa[TB / 64];
+#pragma unroll
+  for (int j = 0; j < TA / 64; ++j) {
+    const int l = 8 * (wave + 8 * j) + (lane >> 3), part = l / (16 * FM), i = l / 16 % FM, q = l % 16;
+    ob[j] = __umul24(static_cast<uint32_t>(min(part * (16 * FM) + q * FM + i, lim_n)), kpb) +
+            static_cast<uint32_t>((lane & 7) ^ ((q >> 1) & 7)) * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < TB / 64; ++j) {
+    const int l = 8 * (wave + 8 * j) + (lane >> 3), part = l / (16 * FN), i = l / 16 % FN, q = l % 16;
+    oa[j] = __umul24(static_cast<uint32_t>(min(part * (16 * FN) + q * FN + i, lim_t)), kpb) +
+            static_cast<uint32_t>((lane & 7) ^ ((q >> 1) & 7)) * 16;
+  }
+  const uint8_t *const gb = p.b + n0 * kpb, *const ga = static_cast<const uint8_t *>(p.a) + t0 * kpb;
+  // scales, 16 bytes a lane: the weight's [block][output], then the rows'
+  const int s16 = wave * kScaleLanes + lane, s_rows = s16 - TA / 2;
+  const uint8_t *const gs = s16 < TA / 2 ? p.sb + s16 / (TA / 16) * rb + min(n0 + s16 % (TA / 16) * 16, rb - 16)
+                                         : p.sa + s_rows / (TB / 16) % kStepBlocks * ra + min(t0 + s_rows % (TB / 16) * 16, ra - 16);
+  const int64_t gs_step = (s16 < TA / 2 ? rb : ra) * kStepBlocks;
+  auto issue = [&](int kb) {
+    lds_char *const st = lds + static_cast<uint32_t>(kb) % kMidStages * kStage;
+    const int64_t k = min(kb, w.end - 1);
+    auto piece = [&](const uint8_t *src, int at) {
+      __builtin_amdgcn_global_load_lds((const void *)src, (__attribute__((address_space(3))) void *)(st + at), 16, 0, 0);
+    };
+#pragma unroll
+    for (int j = 0; j < TA / 64; ++j) piece(gb + k * kRowBytes + ob[j], (wave + 8 * j) * 1024);
+#pragma unroll
+    for (int j = 0; j < TB / 64; ++j) piece(ga + k * kRowBytes + oa[j], kRows + (wave + 8 * j) * 1024);
+    if (lane < kScaleLanes) piece(gs + k * gs_step, kScaleB + wave * (kScaleLanes * 16));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // this lane's block of its half, chunk half * 4 + g4
+  const int block = 4 * half + g4;
+  const uint32_t at = static_cast<uint32_t>(r16 * kRowBytes + ((block ^ (r16 >> 1)) & 7) * 16);
+  u32x4 fb[2][FM], fa[2][FN];
+  uint32_t sb[2], sa[2];
+  auto read = [&](auto set, int kb) {
+    const lds_char *const st = lds + static_cast<uint32_t>(kb) % kMidStages * kStage;
+    sb[set] = *(const lds_u32 *)(st + kScaleB + block * TA + wm * (16 * FM) + r16 * FM);
+    if constexpr (FN == 4)
+      sa[set] = *(const lds_u32 *)(st + kScaleA + block * TB + wn * (16 * FN) + r16 * FN);
+    else
+      sa[set] = *(const lds_u16 *)(st + kScaleA + block * TB + wn * (16 * FN) + r16 * FN);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fb[set][i] = *(const lds_u32x4 *)(st + at + (wm * FM + i) * (16 * kRowBytes));
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fa[set][j] = *(const lds_u32x4 *)(st + kRows + at + (wn * FN + j) * (16 * kRowBytes));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](auto set, int kb) {
+    // this wave's part of the next stage has landed; all waves have used the
+    // fragments of the stage before
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kMidStages - 3) * kLoads) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(kb + kMidStages - 1);
+    // the wait for this step's fragments, before the next step's are read
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(fb[set][i]));
+#pragma unroll
+    for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fa[set][j]));
+    asm volatile("" : "+v"(sb[set]), "+v"(sa[set]));
+    read(std::integral_constant<int, 1 - set>{}, kb + 1);
+    each<FM>([&](auto i) {
+      each<FN>([&](auto j) { acc[i][j] = q4_product<i, j>(fb[set][i], sb[set], fa[set][j], sa[set], acc[i][j]); });
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+#pragma unroll
+  for (int u = 0; u < kMidStages - 1; ++u) issue(w.begin + u);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kMidStages - 2) * kLoads) : "memory");
+  read(even, w.begin);
+  for (int kb = w.begin; kb < w.end; kb += 2) {
+    step(even, kb);
+    if (kb + 1 == w.end) break;
+    step(odd, kb + 1);
+  }
+  // every wave has read its last stage, and the loads that the last steps repeated
+  // have landed
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  constexpr int kSlot = FM * FN / 2 * 1024;
+  static_assert(8 * kSlot <= kMidStages * kStage);
+  exchange_halves<FM, FN>(acc, half, lds + wave * kSlot, lds + (wave ^ 4) * kSlot);
+  const TileOut o = tile_out(w, TA, TB, p.base, p.out, p.out_dt, p.rows, p.outs, p.ws);
+#pragma unroll
+  for (int j = 0; j < FN / 2; ++j) {
+    const int r = wn * (16 * FN) + r16 * FN + half * (FN / 2) + j;
+    if (r >= o.rows) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // eight consecutive outputs of the lane's sixteen
+      const int c = wm * (16 * FM) + g4 * (4 * FM) + h * 8;
+      float run[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) run[e] = acc[(h * 8 + e) % FM][j][(h * 8 + e) / FM];
+      finish_run<8>(o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
+    }
+  }
+}
+
 // A sum of nothing: out = base, or zero.
 __global__ __launch_bounds__(256) void q4_empty_kernel(Q4Product p) {
   const int64_t n = p.rows * p.outs;
@@ -371,7 +512,7 @@ __global__ __launch_bounds__(256) void q4_empty_kernel(Q4Product p) {
 }
 
 constexpr std::initializer_list<TileCost> kCosts = {
-    {256, 256, 1, 1.2f, 1.85f}, {128, 256, 1, 0.85f, 1.04f}, {128, 128, 2, 0.7f, 1.15f}};
+    {256, 256, 1, 1.2f, 1.85f}, {128, 256, 1, 0.85f, 1.04f}, {128, 128, 1, 0.44f, 0.58f}, {128, 64, 1, 0.34f, 0.4f}};
 
 // How a product runs: streamed (row blocks, output blocks and waves of a
 // work-group) or in tiles.
@@ -417,9 +558,15 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
   return pl;
 }
 
-template <int TA, int TB>
+template <int TA>
 hipError_t launch_tiles(const Q4Product &p, const TileSplit &sp, hipStream_t st) {
-  hipLaunchKernelGGL((q4_tile_kernel<TA, TB>), dim3(sp.whole + sp.tail * sp.pieces), dim3(kTileThreads), 0, st, p, sp);
+  hipLaunchKernelGGL(q4_tile_kernel<TA>, dim3(sp.whole + sp.tail * sp.pieces), dim3(kTileThreads), 0, st, p, sp);
+  return hipGetLastError();
+}
+
+template <int TB>
+hipError_t launch_mid(const Q4Product &p, const TileSplit &sp, hipStream_t st) {
+  hipLaunchKernelGGL(q4_mid_kernel<TB>, dim3(sp.whole + sp.tail * sp.pieces), dim3(kMidThreads), 0, st, p, sp);
   return hipGetLastError();
 }
 
@@ -463,9 +610,10 @@ hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
   if (pl.nt == 2) return launch_stream<2>(p, pl, st);
   if (pl.nt == 4) return launch_stream<4>(p, pl, st);
   const TileSplit &sp = pl.split;
-  const hipError_t e = sp.ta == 256   ? launch_tiles<256, 256>(p, sp, st)
-                       : sp.tb == 256 ? launch_tiles<128, 256>(p, sp, st)
-                                      : launch_tiles<128, 128>(p, sp, st);
+  const hipError_t e = sp.ta == 256   ? launch_tiles<256>(p, sp, st)
+                       : sp.tb == 256 ? launch_tiles<128>(p, sp, st)
+                       : sp.tb == 128 ? launch_mid<128>(p, sp, st)
+                                      : launch_mid<64>(p, sp, st);
   if (e != hipSuccess || sp.pieces == 1) return e;
   return launch_q8_reduce(static_cast<const float *>(p.ws), sp, p.rows, p.outs, p.base, p.out, p.out_dt, st);
 }

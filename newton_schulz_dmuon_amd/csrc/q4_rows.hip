@@ -13,6 +13,7 @@
 // then holds four consecutive outputs of one row.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "q4_device.h"
 
@@ -172,8 +173,8 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
 
 // ---- tiles: many rows ----
 //
-// One work-group of 8 waves (2 x 4) computes TA outputs of the weight by TB rows;
-// each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 64 elements per step: 128
+// One work-group of 8 waves (2 x 4) computes TA (128 or 256) outputs of the weight
+// by 256 rows, TB below; each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 64 elements per step: 128
 // bytes of a row, and a quarter of the 256 codes (128 bytes) that a stage of the
 // weight holds.  Both come into LDS by LDS-bound loads (16 bytes a lane, 128-byte
 // rows, the 16-byte chunk XORed with (row / 2) mod 8, which keeps the fragment reads
@@ -184,15 +185,15 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
 //
 // A lane's 16 codes of a step are k = 16 g4 + 0 .. 15, eight of them an instruction.
 // The order of rows in LDS is that of the 4-bit product's tiles.
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 512, kTileRows = 256;
 constexpr int kRowBytes = 128;
 constexpr int kStep = 64, kStageSteps = kQ4Pad / kStep;
 constexpr int kStageBlocks = kQ4Pad / kQ4Block;
 
-template <int TA, int TB>
+template <int TA>
 __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Product &p, const Rows &x, int64_t n0,
-                                             int64_t t0, int kbeg, int kend, f32x4 (&acc)[TA / 32][TB / 64]) {
-  constexpr int FM = TA / 32, FN = TB / 64;
+                                             int64_t t0, int kbeg, int kend, f32x4 (&acc)[TA / 32][kTileRows / 64]) {
+  constexpr int TB = kTileRows, FM = TA / 32, FN = TB / 64;
   // two stages of the weight with its scales (each half's [block][output]), two
   // of the rows
   constexpr int kScales = TA * kRowBytes, kWeight = kScales + TA * kStageBlocks, kRows = TB * kRowBytes;
@@ -311,15 +312,15 @@ __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Produc
   if (wm == 0) barrier();
 }
 
-template <int TA, int TB>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(TB == 256 ? 2 : 4)))
+template <int TA>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
-  constexpr int FM = TA / 32, FN = TB / 64;
+  constexpr int TB = kTileRows, FM = TA / 32, FN = TB / 64;
   __shared__ __attribute__((aligned(1024))) char smem[2 * (TA * (kRowBytes + kStageBlocks) + TB * kRowBytes)];
   const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
   const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
   f32x4 acc[FM][FN];
-  q4_rows_tile<TA, TB>((lds_char *)smem, p, x, n0, t0, w.begin, w.end, acc);
+  q4_rows_tile<TA>((lds_char *)smem, p, x, n0, t0, w.begin, w.end, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
@@ -339,8 +340,175 @@ void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
   }
 }
 
+// ---- small tiles: a deep ring ----
+//
+// 128 outputs by TB (64 or 128) rows, one work-group a CU, for launches of few tiles,
+// which the latency of a step bounds.  Eight waves: four parts of the tile, of 64 x
+// 64 or 32 x 64, and two halves of a step's 128 elements, whose sums are added at the
+// end (each code is then expanded by half as many waves).  Two rings, a longer one of
+// the weight, which comes from memory, and one of the rows, which come from L2: a
+// step waits for the next one's stage, loaded as many steps ago as the ring allows,
+// meets the other waves once, loads the stages that all of them have left, reads the
+// next step's fragments and multiplies its own.  An output's codes are 64 bytes of a
+// stage, their 16-byte chunks XORed with (output / 4) mod 4, a row's elements 256
+// bytes, their chunks XORed with the row.
+//
+// Block i, row q of a wave's weight part holds output q * FM + i, block j, column r
+// of its rows row r * FN + j.
+constexpr int kMidThreads = 512, kMidStep = 128;
+
+template <int TB>
+__global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
+  constexpr int TA = 128, WN = TB / 64, WM = 4 / WN;
+  constexpr int FM = TA / WM / 16, FN = 4, kBlocks = kMidStep / kQ4Block;
+  // stages of the weight (codes, then scales) and of the rows
+  constexpr int kWeightStages = 6, kRowStages = TB == 128 ? 3 : 4;
+  constexpr int kScales = TA * kMidStep / 2, kWeight = kScales + TA * kBlocks, kRows = TB * kMidStep * 2;
+  constexpr int kRowLoads = TB / 32, kLoads = kRowLoads + 2;  // vector loads a wave and step
+  __shared__ __attribute__((aligned(1024))) char smem[kRowStages * kRows + kWeightStages * kWeight];
+  lds_char *const lds = (lds_char *)smem, *const lds_w = lds + kRowStages * kRows;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2, wm = (wave & 3) / WN, wn = (wave & 3) % WN, r16 = lane & 15, g4 = lane >> 4;
+  const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
+  const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
+  const int begin = w.begin * (kQ4Pad / kMidStep);
+  const int end = min(w.end * (kQ4Pad / kMidStep), static_cast<int>(x.ld / kMidStep));
+  const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
+  const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
+  const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TA - 1)));
+  const int lim_t = static_cast<int>(min(p.rows - 1 - t0, static_cast<int64_t>(TB - 1)));
+  // a wave's load of codes fills LDS rows 16 wave + l / 4, physical chunk l % 4; its
+  // load j of the rows LDS rows 4 (wave + 8 j) + l / 16, physical chunk l % 16
+  uint32_t ob, oa[kRowLoads];
+  {
+    const int part = wave / FM, i = wave % FM, q = lane >> 2;
+    ob = __umul24(static_cast<uint32_t>(min(part * (16 * FM) + q * FM + i, lim_n)), kpb) +
+         static_cast<uint32_t>((lane & 3) ^ ((q >> 2) & 3)) * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < kRowLoads; ++j) {
+    const int l = 4 * (wave + 8 * j) + (lane >> 4), part = l / (16 * FN), i = l / 16 % FN, q = l % 16;
+    oa[j] = __umul24(static_cast<uint32_t>(min(part * (16 * FN) + q * FN + i, lim_t)), ldb) +
+            static_cast<uint32_t>((lane & 15) ^ q) * 16;
+  }
+  const uint8_t *const gb = p.b + n0 * kpb, *const ga = x.x + t0 * ldb;
+  // scales, 16 bytes a lane and four lanes a wave: [block][output]
+  const int s16 = wave * 4 + (lane & 3);
+  const uint8_t *const gs = p.sb + s16 / (TA / 16) * rb + min(n0 + s16 % (TA / 16) * 16, rb - 16);
+  auto piece = [&](const uint8_t *src, lds_char *to) {
+    __builtin_amdgcn_global_load_lds((const void *)src, (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+  };
+  auto issue_rows = [&](int ks) {
+    lds_char *const st = lds + static_cast<uint32_t>(ks) % kRowStages * kRows;
+    const int64_t k = min(ks, end - 1);
+#pragma unroll
+    for (int j = 0; j < kRowLoads; ++j) piece(ga + k * (kMidStep * 2) + oa[j], st + (wave + 8 * j) * 1024);
+  };
+  auto issue_weight = [&](int ks) {
+    lds_char *const st = lds_w + static_cast<uint32_t>(ks) % kWeightStages * kWeight;
+    const int64_t k = min(ks, end - 1);
+    piece(gb + k * (kMidStep / 2) + ob, st + wave * 1024);
+    if (lane < 4) piece(gs + k * kBlocks * rb, st + kScales + wave * 64);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // this lane's sixteen elements of its half: k = 16 g4 + 0 .. 15
+  const int block = 2 * half + (g4 >> 1);
+  const int at_b = (wm * (16 * FM) + r16) * 64 + ((block ^ (r16 >> 2)) & 3) * 16 + (g4 & 1) * 8;
+  const int at_s = kScales + block * TA + wm * (16 * FM) + r16 * FM;
+  u32x2 fb[2][FM];
+  u32x4 fa[2][FN][2];
+  uint32_t sb[2];
+  auto read = [&](auto set, int ks) {
+    const lds_char *const sw = lds_w + static_cast<uint32_t>(ks) % kWeightStages * kWeight;
+    const lds_char *const sx = lds + static_cast<uint32_t>(ks) % kRowStages * kRows + (wn * (16 * FN) + r16) * 256;
+    if constexpr (FM == 4)
+      sb[set] = *(const lds_u32 *)(sw + at_s);
+    else
+      sb[set] = *(const lds_u16 *)(sw + at_s);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fb[set][i] = *(const lds_u32x2 *)(sw + at_b + i * (16 * 64));
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        fa[set][j][d] = *(const lds_u32x4 *)(sx + j * (16 * 256) + (((8 * half + 2 * g4 + d) ^ r16) & 15) * 16);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](auto set, int ks) {
+    // this wave's part of the next stages has landed (the rows' were loaded
+    // kRowStages - 2 steps ago, before that step's part of the weight, the weight's
+    // earlier); all waves have used the fragments of the stages before
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRowStages - 3) * kLoads + 2) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue_rows(ks + kRowStages - 1);
+    issue_weight(ks + kWeightStages - 1);
+    // the wait for this step's fragments, before the next step's are read
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(fb[set][i]));
+#pragma unroll
+    for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fa[set][j][0]), "+v"(fa[set][j][1]));
+    asm volatile("" : "+v"(sb[set]));
+    read(std::integral_constant<int, 1 - set>{}, ks + 1);
+    float s[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) s[i] = q4_half_scale(sb[set] >> (8 * i) & 0xff);
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const bf16x8 xb = q4_expand8(fb[set][i][d], s[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, __builtin_bit_cast(bf16x8, fa[set][j][d]), acc[i][j], 0, 0, 0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  // the weight's stages before the rows', as the steps' waits count on
+#pragma unroll
+  for (int u = 0; u < kWeightStages - 1; ++u) issue_weight(begin + u);
+#pragma unroll
+  for (int u = 0; u < kRowStages - 1; ++u) issue_rows(begin + u);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRowStages - 2) * kRowLoads) : "memory");
+  read(even, begin);
+  for (int ks = begin; ks < end; ks += 2) {
+    step(even, ks);
+    if (ks + 1 == end) break;
+    step(odd, ks + 1);
+  }
+  // every wave has read its last stage, and the loads that the last steps repeated
+  // have landed
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  constexpr int kSlot = FM * FN / 2 * 1024;
+  static_assert(8 * kSlot <= sizeof(smem));
+  exchange_halves<FM, FN>(acc, half, lds + wave * kSlot, lds + (wave ^ 4) * kSlot);
+  const TileOut o = tile_out(w, TA, TB, nullptr, p.out, p.out_dt, p.rows, p.outs, p.ws);
+#pragma unroll
+  for (int j = 0; j < FN / 2; ++j) {
+    const int r = wn * (16 * FN) + r16 * FN + half * (FN / 2) + j;
+    if (r >= o.rows) continue;
+#pragma unroll
+    for (int h = 0; h < FM / 2; ++h) {
+      // eight consecutive outputs of the lane's 4 FM
+      const int c = wm * (16 * FM) + g4 * (4 * FM) + h * 8;
+      float run[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) run[e] = 2.f * acc[(h * 8 + e) % FM][j][(h * 8 + e) / FM];
+      finish_run<8>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
+    }
+  }
+}
+
 constexpr std::initializer_list<TileCost> kCosts = {
-    {256, 256, 1, 4.7f, 6.15f}, {128, 256, 1, 3.2f, 3.5f}, {128, 128, 2, 2.6f, 4.03f}};
+    {256, 256, 1, 4.6f, 5.9f}, {128, 256, 1, 3.2f, 3.5f}, {128, 128, 1, 1.75f, 2.1f}, {128, 64, 1, 0.97f, 1.15f}};
 
 // How a product runs: streamed (output blocks of a work-group) or in tiles; its rows' distance; and the bytes of its workspace's two
 // parts, the padded rows and the pieces' results.
@@ -383,17 +551,22 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
     if (pl.nn) pl.split = TileSplit{};
   }
   // PLAN_HOOK
-  const int64_t step = pl.nn ? kQ4Pad : kStep;
+  const int64_t step = pl.nn ? kQ4Pad : pl.split.tb == 256 ? kStep : kMidStep;
   pl.ld = (inner + step - 1) / step * step;
   if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
   pl.piece_bytes = pl.split.ws_bytes();
   return pl;
 }
 
-template <int TA, int TB>
+template <int TA>
 hipError_t launch_tiles(const Q4Product &p, const Rows &x, const TileSplit &sp, hipStream_t st) {
-  hipLaunchKernelGGL((q4_rows_tile_kernel<TA, TB>), dim3(sp.whole + sp.tail * sp.pieces), dim3(kTileThreads), 0, st, p,
-                     x, sp);
+  hipLaunchKernelGGL(q4_rows_tile_kernel<TA>, dim3(sp.whole + sp.tail * sp.pieces), dim3(kTileThreads), 0, st, p, x, sp);
+  return hipGetLastError();
+}
+
+template <int TB>
+hipError_t launch_mid(const Q4Product &p, const Rows &x, const TileSplit &sp, hipStream_t st) {
+  hipLaunchKernelGGL(q4_rows_mid_kernel<TB>, dim3(sp.whole + sp.tail * sp.pieces), dim3(kMidThreads), 0, st, p, x, sp);
   return hipGetLastError();
 }
 
@@ -435,9 +608,10 @@ hipError_t launch_q4_rows(const Q4Product &args, hipStream_t st) {
   if (pl.nn == 2) return launch_stream<2>(p, x, st);
   if (pl.nn == 4) return launch_stream<4>(p, x, st);
   const TileSplit &sp = pl.split;
-  const hipError_t e = sp.ta == 256   ? launch_tiles<256, 256>(p, x, sp, st)
-                       : sp.tb == 256 ? launch_tiles<128, 256>(p, x, sp, st)
-                                      : launch_tiles<128, 128>(p, x, sp, st);
+  const hipError_t e = sp.ta == 256   ? launch_tiles<256>(p, x, sp, st)
+                       : sp.tb == 256 ? launch_tiles<128>(p, x, sp, st)
+                       : sp.tb == 128 ? launch_mid<128>(p, x, sp, st)
+                                      : launch_mid<64>(p, x, sp, st);
   if (e != hipSuccess || sp.pieces == 1) return e;
   return launch_q8_reduce(static_cast<const float *>(p.ws), sp, p.rows, p.outs, nullptr, p.out, p.out_dt, st);
 }
