@@ -542,7 +542,7 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
   if (rows <= kStreamRows) {
     for (const int nt : {1, 2, 4})
       for (const int nn : {1, 2, 4}) {
-        if (nn == 4 && nt != 4) continue;
+        if (nn != 2 && nn != nt) continue;  // 1 x 1, 1 x 2, 2 x 2, 4 x 2 and 4 x 4
         const float s = stream_us(rows, outs, kp, nt, nn);
         if (s >= us) continue;
         us = s;
@@ -577,22 +577,10 @@ hipError_t launch_stream(const Q4Product &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int NT, int NN>
-hipError_t launch_stream(const Q4Product &p, int waves, hipStream_t st) {
-  if constexpr (NT * NN <= 2)
-    if (waves == 8) {
-      if (NT == 1 && p.rows <= 8) return launch_stream<NT, NN, 8, NT == 1 ? 8 : 16>(p, st);
-      return launch_stream<NT, NN, 8, 16>(p, st);
-    }
-  if (NT == 1 && p.rows <= 8) return launch_stream<NT, NN, 4, NT == 1 ? 8 : 16>(p, st);
-  return launch_stream<NT, NN, 4, 16>(p, st);
-}
-
-template <int NT>
-hipError_t launch_stream(const Q4Product &p, const Plan &pl, hipStream_t st) {
-  if constexpr (NT == 4)
-    if (pl.nn == 4) return launch_stream<4, 4>(p, pl.waves, st);
-  return pl.nn == 2 ? launch_stream<NT, 2>(p, pl.waves, st) : launch_stream<NT, 1>(p, pl.waves, st);
+// One row block: of up to eight rows, eight are loaded.
+template <int NN, int WAVES>
+hipError_t launch_stream(const Q4Product &p, hipStream_t st) {
+  return p.rows <= 8 ? launch_stream<1, NN, WAVES, 8>(p, st) : launch_stream<1, NN, WAVES, 16>(p, st);
 }
 
 }  // namespace
@@ -606,9 +594,9 @@ hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
     return hipGetLastError();
   }
   const Plan pl = plan_of(p.rows, p.outs, p.kp);
-  if (pl.nt == 1) return launch_stream<1>(p, pl, st);
-  if (pl.nt == 2) return launch_stream<2>(p, pl, st);
-  if (pl.nt == 4) return launch_stream<4>(p, pl, st);
+  if (pl.nt == 1) return pl.nn == 2 ? launch_stream<2, 4>(p, st) : pl.waves == 8 ? launch_stream<1, 8>(p, st) : launch_stream<1, 4>(p, st);
+  if (pl.nt == 2) return launch_stream<2, 2, 4, 16>(p, st);
+  if (pl.nt == 4) return pl.nn == 2 ? launch_stream<4, 2, 4, 16>(p, st) : launch_stream<4, 4, 4, 16>(p, st);
   const TileSplit &sp = pl.split;
   const hipError_t e = sp.ta == 256   ? launch_tiles<256>(p, sp, st)
                        : sp.tb == 256 ? launch_tiles<128>(p, sp, st)

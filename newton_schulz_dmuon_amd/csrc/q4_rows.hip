@@ -472,12 +472,17 @@ void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
   };
   constexpr std::integral_constant<int, 0> even{};
   constexpr std::integral_constant<int, 1> odd{};
-  // the weight's stages before the rows', as the steps' waits count on
+  // the steps' waits count on their order of loads: the last stages as the steps
+  // would have loaded them
+  constexpr int kFirst = kWeightStages - kRowStages;
 #pragma unroll
-  for (int u = 0; u < kWeightStages - 1; ++u) issue_weight(begin + u);
+  for (int u = 0; u < kFirst; ++u) issue_weight(begin + u);
 #pragma unroll
-  for (int u = 0; u < kRowStages - 1; ++u) issue_rows(begin + u);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRowStages - 2) * kRowLoads) : "memory");
+  for (int u = 0; u < kRowStages - 1; ++u) {
+    issue_rows(begin + u);
+    issue_weight(begin + kFirst + u);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((kRowStages - 2) * kLoads + 2) : "memory");
   read(even, begin);
   for (int ks = begin; ks < end; ks += 2) {
     step(even, ks);

@@ -336,6 +336,41 @@ def test_large_products(t, n, k):
         check_sum(nsd.q4_weight_grad(d4, z4, out=b, base=b), want_b, mag_b, adds(t), (t, n, k, dtype, "in place"))
 
 
+# (every work-group of the streaming kernels, with rings that turn, and every tile:
+# whole, split, both)
+EVERY_KERNEL = [(10, 33, 1117), (1, 17, 1408), (9, 5, 6797), (1, 30, 4703), (17, 2180, 1248), (1, 5006, 1511), (81, 1457, 1154),
+                (432, 603, 1114), (70, 6226, 1166), (10174, 136, 1161), (6306, 20, 13207), (5629, 676, 4018),
+                (272, 13686, 1182), (6069, 1352, 4022), (1070, 40, 1285), (1289, 10, 4785), (8204, 193, 13635),
+                (1671, 4760, 1199), (6738, 2463, 3873), (4, 20, 1813), (5, 40, 1118), (3, 4108, 1278), (6, 4720, 1383),
+                (9, 10357, 1144), (1, 13032, 1134), (4, 9356, 1472), (5, 9980, 1598), (9283, 4, 6531), (638, 6649, 1798),
+                (3720, 1543, 1202), (10351, 2, 13646), (724, 11302, 1331), (2637, 30, 1245), (12, 1, 13681),
+                (2326, 882, 1510), (6785, 131, 19804), (1208, 13114, 1424)]
+
+
+@pytest.mark.parametrize("t,n,k", EVERY_KERNEL)
+def test_every_kernel(t, n, k):
+    """Against float64 products on the GPU of the values that the codes stand for,
+    onto a base too."""
+    print(f"every kernel {t} {n} {k}", flush=True)
+    torch.manual_seed(t + n)
+    x = (torch.randn(t, k, device="cuda") * torch.exp2(torch.randint(-8, 9, (t, 1), device="cuda"))).to(BF16)
+    w = (0.02 * torch.randn(n, k, device="cuda") * torch.exp2(torch.randint(-8, 9, (1, k), device="cuda"))).to(BF16)
+    x4, w4 = nsd.q4_quantize(x), nsd.q4_quantize_weights([w])[0]
+    wv = unpacked(w4.codes, w4.scales, n, k).t().contiguous()
+    for a, v, count in ((x4, unpacked(x4.codes, x4.scales, t, k), adds(k)), (x, x.double(), k + 25)):
+        want, mag = v @ wv, v.abs() @ wv.abs()
+        for dtype in (BF16, F32):
+            check_sum(nsd.q4_matmul(a, w4, dtype=dtype), want.cpu().numpy(), mag.cpu().numpy(), count, (t, n, k, dtype))
+    # the same sums as a weight gradient: t outputs by n columns over k tokens
+    d4, z4 = nsd.Q4Matrix(k, t, None, None, x4.codes, x4.scales), nsd.Q4Matrix(k, n, None, None, w4.codes, w4.scales)
+    v = unpacked(x4.codes, x4.scales, t, k)
+    want, mag = v @ wv, v.abs() @ wv.abs()
+    for dtype in (BF16, F32):
+        b = torch.randn(t, n, device="cuda").to(dtype)
+        want_b, mag_b = (want + b.double()).cpu().numpy(), (mag + b.double().abs()).cpu().numpy()
+        check_sum(nsd.q4_weight_grad(d4, z4, base=b), want_b, mag_b, adds(k), (t, n, k, dtype, "onto a base"))
+
+
 def test_no_rows():
     print("no rows", flush=True)
     rng = np.random.default_rng(1)
