@@ -57,6 +57,19 @@ def _raw_stream(index: int) -> int:
     return _raw(index)
 
 
+_device = None
+
+
+def _current_device() -> int:
+    """``torch.cuda.current_device()`` for a caller that holds a tensor on a GPU,
+    without the check that CUDA is initialised."""
+    global _device
+    if _device is None:
+        import torch
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
+
+
 _NO_CONTEXT = contextlib.nullcontext()
 
 

@@ -32,6 +32,7 @@ gives the same bits.
 
 from __future__ import annotations
 
+import ctypes
 from typing import List, Optional, Sequence
 
 from . import _lib
@@ -106,16 +107,13 @@ def _check_out(q: Q4Matrix, rows: int, cols: int, device) -> None:
         _check_form(q.codes_t, q.scales_t, cols, rows, "out's transpose", device)
 
 
-def _quantize(xs, shapes, randoms, out, made, device, stream) -> None:
-    """One launch over matrices whose arguments have been checked."""
-    arr = (Q4SourceDesc * len(xs))()
-    for i, (x, (rows, cols), r, q) in enumerate(zip(xs, shapes, randoms, out)):
-        arr[i] = Q4SourceDesc(_ptr(x), _dtype_code(x), 0, rows, cols, _ptr(r), *(_ptr(t) for t in q.tensors()))
-        if stream is not None:
-            _keep(device, stream, [t for t in q.tensors() if t is not None], made, (x, r))
-    _run(load().dmuon_q4_quantize, device, stream, arr, len(xs))
-    for (rows, cols), q in zip(shapes, out):
-        q.rows, q.cols = rows, cols
+def _source(x, dt: int, rows: int, cols: int, random, q: Q4Matrix) -> Q4SourceDesc:
+    """The descriptor of a matrix whose arguments have been checked."""
+    codes, codes_t = q.codes, q.codes_t
+    return Q4SourceDesc(x.data_ptr(), dt, 0, rows, cols, None if random is None else random.data_ptr(),
+                        None if codes is None else codes.data_ptr(), None if codes is None else q.scales.data_ptr(),
+                        None if codes_t is None else codes_t.data_ptr(),
+                        None if codes_t is None else q.scales_t.data_ptr())
 
 
 def q4_quantize(x, transposed: bool = False, random=None, plain: bool = True, out: Optional[Q4Matrix] = None,
@@ -133,7 +131,7 @@ def q4_quantize(x, transposed: bool = False, random=None, plain: bool = True, ou
         _check_stream(device, stream)
     if random is not None:
         _check_tensor(random, "random", x.shape, torch.uint8, device)
-    _dtype_code(x)
+    dt = _dtype_code(x)
     _ptr(x)
     made = out is None
     if made:
@@ -143,7 +141,10 @@ def q4_quantize(x, transposed: bool = False, random=None, plain: bool = True, ou
             out = Q4Matrix.empty(rows, cols, device, plain, transposed)
     else:
         _check_out(out, rows, cols, device)
-    _quantize([x], [(rows, cols)], [random], [out], made, device, stream)
+    if stream is not None:
+        _keep(device, stream, [t for t in out.tensors() if t is not None], made, (x, random))
+    _run(load().dmuon_q4_quantize, device, stream, ctypes.byref(_source(x, dt, rows, cols, random, out)), 1)
+    out.rows, out.cols = rows, cols
     return out
 
 
@@ -179,7 +180,14 @@ def q4_quantize_weights(params: Sequence, out: Optional[Sequence[Q4Matrix]] = No
             raise _invalid(f"{len(out)} results for {n} matrices")
         for p, q in zip(params, out):
             _check_out(q, p.shape[0], p.shape[1], device)
-    _quantize(params, [tuple(p.shape) for p in params], [None] * n, out, made, device, stream)
+    arr = (Q4SourceDesc * n)()
+    for i, (p, q) in enumerate(zip(params, out)):
+        arr[i] = _source(p, _dtype_code(p), p.shape[0], p.shape[1], None, q)
+        if stream is not None:
+            _keep(device, stream, [t for t in q.tensors() if t is not None], made, (p,))
+    _run(load().dmuon_q4_quantize, device, stream, arr, n)
+    for p, q in zip(params, out):
+        q.rows, q.cols = p.shape
     return out
 
 

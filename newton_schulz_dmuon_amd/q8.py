@@ -38,7 +38,7 @@ from typing import List, Optional, Sequence
 
 from . import _lib
 from ._lib import DmuonError, Q8WeightDesc, check, load
-from .api import Workspace, _allocating, _dtype_code, _mark_used, _ptr, _raw_stream
+from .api import Workspace, _allocating, _current_device, _dtype_code, _mark_used, _ptr, _raw_stream
 
 BLOCK = 128
 
@@ -150,7 +150,7 @@ def _run(fn, device, stream, *args) -> None:
         handle = _raw_stream(index)
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
