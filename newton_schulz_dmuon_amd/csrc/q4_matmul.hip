@@ -534,7 +534,7 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
 // Rows up to which it is considered.
 constexpr int64_t kStreamRows = 1024;
 
-Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
+Plan make_plan(int64_t rows, int64_t outs, int64_t kp) {
   Plan pl{};
   if (rows == 0 || kp == 0) return pl;
   float us;
@@ -556,6 +556,22 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
   }
   // PLAN_HOOK
   return pl;
+}
+
+// ... kept for the next call, which asks for the same sizes again: the workspace's
+// bytes, the check of the workspace and the launch of one product.
+Plan plan_of(int64_t rows, int64_t outs, int64_t kp) {
+  static thread_local struct {
+    int64_t rows, outs, kp;
+    Plan plan;  // of no rows, as at first, all zero
+  } last;
+  if (last.rows != rows || last.outs != outs || last.kp != kp) {
+    last.plan = make_plan(rows, outs, kp);
+    last.rows = rows;
+    last.outs = outs;
+    last.kp = kp;
+  }
+  return last.plan;
 }
 
 template <int TA>

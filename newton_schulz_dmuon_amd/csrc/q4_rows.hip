@@ -540,7 +540,7 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nn) {
 // Rows up to which it is considered.
 constexpr int64_t kStreamRows = 1024;
 
-Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
+Plan make_plan(int64_t rows, int64_t outs, int64_t inner) {
   Plan pl{};
   if (rows == 0) return pl;
   const int64_t kp = (inner + kQ4Pad - 1) / kQ4Pad * kQ4Pad;
@@ -561,6 +561,22 @@ Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
   if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
   pl.piece_bytes = pl.split.ws_bytes();
   return pl;
+}
+
+// ... kept for the next call, which asks for the same sizes again: the workspace's
+// bytes, the check of the workspace and the launch of one product.
+Plan plan_of(int64_t rows, int64_t outs, int64_t inner) {
+  static thread_local struct {
+    int64_t rows, outs, inner;
+    Plan plan;  // of no rows, as at first, all zero
+  } last;
+  if (last.rows != rows || last.outs != outs || last.inner != inner) {
+    last.plan = make_plan(rows, outs, inner);
+    last.rows = rows;
+    last.outs = outs;
+    last.inner = inner;
+  }
+  return last.plan;
 }
 
 template <int TA>
