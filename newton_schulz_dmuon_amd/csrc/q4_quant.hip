@@ -22,10 +22,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
+// Rows read back per launch: its threads along the grid stay below 2^32.
+constexpr int64_t kLaunchRows = int64_t(1) << 28;
 
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 // eight bytes at any address
 typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
 typedef __attribute__((address_space(1))) u32x2_at1 g_u32x2_at1;
+typedef u32x2 u32x2_at4 __attribute__((aligned(4)));
+typedef __attribute__((address_space(1))) u32x2_at4 g_u32x2_at4;
 
 // The scale byte of a block whose largest magnitude has these fp32 bits.
 __device__ __forceinline__ int scale_byte(uint32_t amax) {
@@ -57,26 +62,27 @@ template <bool F32> struct Eight {
       for (int k = 0; k < 4; ++k) w[k] = a[k];
     }
   }
-  // the first `left` of them, zeros behind
-  __device__ __forceinline__ void load_some(const void *x, int64_t i, int64_t left) {
+  // element by element, each at its own place; elements `left` on are zero
+  template <typename P>
+  __device__ __forceinline__ void load_each(const void *x, P place, int64_t left) {
+    uint32_t e[8];
 #pragma unroll
-    for (int k = 0; k < (F32 ? 8 : 4); ++k) w[k] = 0;
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (F32)
+        e[k] = ((const g_u32 *)x)[place(k)];
+      else
+        e[k] = ((const g_u16 *)x)[place(k)];
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < left) {
-        if constexpr (F32)
-          w[k] = ((const g_u32 *)x)[i + k];
-        else
-          w[k / 2] |= static_cast<uint32_t>(((const g_u16 *)x)[i + k]) << (16 * (k % 2));
-      }
+    for (int k = 0; k < 8; ++k) e[k] = k < left ? e[k] : 0;
+#pragma unroll
+    for (int k = 0; k < (F32 ? 8 : 4); ++k) w[k] = F32 ? e[k] : e[2 * k % 8] | e[(2 * k + 1) % 8] << 16;
   }
-  __device__ __forceinline__ float get(int k) const {
-    if constexpr (F32) return __uint_as_float(w[k]);
-    return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  __device__ __forceinline__ void zero_unless(bool is) {
+#pragma unroll
+    for (int k = 0; k < (F32 ? 8 : 4); ++k) w[k] = is ? w[k] : 0;
   }
 };
-
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // Magnitudes as ordered bits: fp32's, or two bf16's in the halves of a word.
 template <bool F32> __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & (F32 ? 0x7fffffffu : 0x7fff7fffu); }
@@ -99,37 +105,85 @@ template <bool F32> __device__ __forceinline__ uint32_t stride4_max(uint32_t v) 
   return larger_dpp<F32, 0x128>(larger_dpp<F32, 0x124>(v));
 }
 
-// A value times 2^-e rounded by a random byte n: in units of 2^-10, of which a step
-// between codes has 512, 1024 or 2048 (values below 2, 4 and 6), up iff what lies
-// above the code below is at least 255.5 - n of 256 parts.  Cutting the value to
+// Two values times 2^-e rounded by their random bytes n: in units of 2^-10, of which
+// a step between codes has 512, 1024 or 2048 (values below 2, 4 and 6), up iff what
+// lies above the code below is at least 255.5 - n of 256 parts.  Cutting a value to
 // whole units changes no comparison, since every threshold is a whole number of
-// them.  unit: 2^(10 - e).
-__device__ __forceinline__ uint32_t random_code(float v, float unit, uint32_t n) {
-  const uint32_t u = static_cast<uint32_t>(__builtin_fabsf(v) * unit);
-  const uint32_t wide = min(u >> 11, 2u);
-  return ((u + ((2 * n + 1) << wide)) >> (9 + wide)) + 2 * wide;
+// them.  more * unit: 2^(10 - e), in two factors, of which fp32 holds each.
+__device__ __forceinline__ u16x2 random_codes(float a, float b, float more, float unit, u16x2 n) {
+  const u16x2 u = {static_cast<unsigned short>(static_cast<uint32_t>(__builtin_fabsf(a) * more * unit)),
+                   static_cast<unsigned short>(static_cast<uint32_t>(__builtin_fabsf(b) * more * unit))};
+  const u16x2 wide = __builtin_elementwise_min(u >> 11, u16x2{2, 2});
+  return ((u + ((n + n + 1) << wide)) >> (wide + 9)) + (wide + wide);
 }
 
-// The codes of eight elements, the first in the lowest four bits.  n: their random
-// bytes.
-template <bool RANDOM>
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], int byte, u32x2 n) {
+// Four pairs of elements, as the halves of a word in bf16 or as two words in fp32.
+template <bool F32> struct Pairs {
+  uint32_t w[F32 ? 8 : 4];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (F32) return __uint_as_float(w[k % 8]);
+    return __uint_as_float(k % 2 ? w[k / 2 % 4] & 0xffff0000u : w[k / 2 % 4] << 16);
+  }
+};
+
+// The codes of eight elements, the first in the lowest four bits.  n(k): the random
+// bytes of pair k, in the halves of a word.
+template <bool F32, bool RANDOM, typename N>
+__device__ __forceinline__ uint32_t codes8(const Pairs<F32> &x, int byte, N n) {
   uint32_t w = 0;
   if constexpr (RANDOM) {
-    // 2^(10 - e) in two factors, of which fp32 holds each
-    const float unit = __uint_as_float(static_cast<uint32_t>(min(254 + 10 - byte, 254)) << 23);
-    const float more = byte < 10 ? __uint_as_float(static_cast<uint32_t>(127 + 10 - byte) << 23) : 1.f;
+    const float unit = __uint_as_float(static_cast<uint32_t>(min(264 - byte, 254)) << 23);
+    const float more = __uint_as_float(static_cast<uint32_t>(127 + max(10 - byte, 0)) << 23);
+    uint32_t two[4];  // a pair's two codes in the lowest byte
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      w |= (random_code(v[k] * more, unit, n[k / 4] >> (8 * (k % 4)) & 0xff) | (__float_as_uint(v[k]) >> 31 << 3)) << (4 * k);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t c = __builtin_bit_cast(
+          uint32_t, random_codes(x.get(2 * k), x.get(2 * k + 1), more, unit, __builtin_bit_cast(u16x2, n(k))));
+      const uint32_t sign = F32 ? __builtin_amdgcn_perm(x.w[(2 * k + 1) % (F32 ? 8 : 4)], x.w[2 * k % (F32 ? 8 : 4)], 0x07060302u)
+                                : x.w[k];  // in bits 15 and 31
+      const uint32_t s = (sign >> 12 & 0x00080008u) | c;
+      two[k] = s | s >> 12;
+    }
+    w = __builtin_amdgcn_perm(__builtin_amdgcn_perm(two[3], two[2], 0x0c0c0400u),
+                              __builtin_amdgcn_perm(two[1], two[0], 0x0c0c0400u), 0x05040100u);
+  } else if constexpr (F32) {
+    const float s = scale_of(byte);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x.get(0), x.get(1), s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x.get(2), x.get(3), s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x.get(4), x.get(5), s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x.get(6), x.get(7), s, 3);
   } else {
     const float s = scale_of(byte);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, x.w[0]), s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, x.w[1]), s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, x.w[2]), s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, x.w[3]), s, 3);
   }
   return byte == kQ4Nan ? 0u : w;
+}
+
+// Eight bytes from `at` on, of eight rows `step` apart.  Loads at any byte's address
+// are slow (8192 x 4095 elements 61 us): whole words are loaded and shifted, where
+// none of them lies behind the `size` bytes.
+__device__ __forceinline__ void load_bytes(const uint8_t *p, int64_t at, int64_t step, int64_t size, u32x2 (&n)[8]) {
+  if ((step & 7) == 0 || at + 7 * step + 12 > size) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) n[r] = *(const g_u32x2_at1 *)(p + at + r * step);
+    return;
+  }
+  u32x2 lo[8];
+  uint32_t hi[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int64_t word = (at + r * step) & ~int64_t(3);
+    lo[r] = *(const g_u32x2_at4 *)(p + word);
+    hi[r] = *(const g_u32 *)(p + word + 8);
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const uint32_t shift = static_cast<uint32_t>(at + r * step) & 3;
+    n[r] = u32x2{__builtin_amdgcn_alignbyte(lo[r].y, lo[r].x, shift), __builtin_amdgcn_alignbyte(hi[r], lo[r].y, shift)};
+  }
 }
 
 // Eight scale bytes as two words.
@@ -164,22 +218,27 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
   if (r0 + 8 <= rows && c0 + 8 <= cols) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) x[r].load(b.x[mi], (r0 + r) * cols + c0);
+    if constexpr (RANDOM) load_bytes(b.random[mi], r0 * cols + c0, cols, rows * cols, n);
+  } else if (c0 + 8 <= cols) {
+    // rows behind the last: the last one's elements, then zeros
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r].load(b.x[mi], min(r0 + r, rows - 1) * cols + c0);
     if constexpr (RANDOM)
 #pragma unroll
-      for (int r = 0; r < 8; ++r) n[r] = *(const g_u32x2_at1 *)(b.random[mi] + (r0 + r) * cols + c0);
+      for (int r = 0; r < 8; ++r) n[r] = *(const g_u32x2_at1 *)(b.random[mi] + min(r0 + r, rows - 1) * cols + c0);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r].zero_unless(r0 + r < rows);
   } else {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int64_t left = r0 + r < rows ? cols - c0 : 0;
-      if (left >= 8)
-        x[r].load(b.x[mi], (r0 + r) * cols + c0);
-      else
-        x[r].load_some(b.x[mi], (r0 + r) * cols + c0, left);
-      n[r] = u32x2{0, 0};
-      if constexpr (RANDOM)
+      const int64_t row = min(r0 + r, rows - 1) * cols;
+      auto place = [&](int k) { return row + min(c0 + k, cols - 1); };
+      x[r].load_each(b.x[mi], place, r0 + r < rows ? cols - c0 : 0);
+      if constexpr (RANDOM) {
+        n[r] = u32x2{0, 0};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < left) n[r][k / 4] |= static_cast<uint32_t>(((const g_u8 *)b.random[mi])[(r0 + r) * cols + c0 + k]) << (8 * (k % 4));
+        for (int k = 0; k < 8; ++k) n[r][k / 4] |= static_cast<uint32_t>(((const g_u8 *)b.random[mi])[place(k)]) << (8 * (k % 4));
+      }
     }
   }
   constexpr int W = F32 ? 8 : 4;
@@ -202,10 +261,13 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
   if (codes) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      float v[8];
+      Pairs<F32> v;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = x[r].get(k);
-      const uint32_t w = codes8<RANDOM>(v, bytes[r], n[r]);
+      for (int k = 0; k < W; ++k) v.w[k] = x[r].w[k];
+      // bytes 2 k and 2 k + 1 of the row's
+      const uint32_t w = codes8<F32, RANDOM>(v, bytes[r], [&](int k) {
+        return __builtin_amdgcn_perm(0, n[r][k / 2], k % 2 ? 0x0c030c02u : 0x0c010c00u);
+      });
       if (r0 + r < rows && c0 < kp) *(g_u32 *)(codes + (r0 + r) * (kp / 2) + c0 / 2) = w;
     }
     if ((lane & 3) == 0 && r0 < r16 && c0 < kp) *(g_u32x2 *)(b.scales[mi] + c0 / kQ4Block * r16 + r0) = pack8(bytes);
@@ -217,14 +279,18 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     bytes[k] = scale_byte(F32 ? col_max[k % W] : k % 2 ? col_max[k / 2 % W] & 0xffff0000u : col_max[k / 2 % W] << 16);
-    float v[8];
-    u32x2 nc = {0, 0};
+    Pairs<F32> v;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      v[r] = x[r].get(k);
-      if constexpr (RANDOM) nc[r / 4] |= (n[r][k / 4] >> (8 * (k % 4)) & 0xff) << (8 * (r % 4));
+    for (int r = 0; r < W; ++r) {
+      if constexpr (F32)
+        v.w[r] = x[r].w[k];
+      else
+        v.w[r] = __builtin_amdgcn_perm(x[2 * r + 1].w[k / 2], x[2 * r].w[k / 2], k % 2 ? 0x07060302u : 0x05040100u);
     }
-    *(lds_u32 *)(lds + (cl + k) * kPitch + rl / 2) = codes8<RANDOM>(v, bytes[k], nc);
+    // byte k of two rows'
+    *(lds_u32 *)(lds + (cl + k) * kPitch + rl / 2) = codes8<F32, RANDOM>(v, bytes[k], [&](int q) {
+      return __builtin_amdgcn_perm(n[2 * q + 1][k / 4], n[2 * q][k / 4], 0x0c040c00u + (k % 4) * 0x00010001u);
+    });
   }
   if ((lane & 12) == 0 && c0 < c16 && r0 < rp) *(g_u32x2 *)(b.scales_t[mi] + r0 / kQ4Block * c16 + c0) = pack8(bytes);
   __syncthreads();
@@ -260,12 +326,12 @@ hipError_t launch_quantise(const Q4Batch &b, hipStream_t st) {
 // values round to and which becomes infinite.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void q4_dequantise_kernel(const uint8_t *__restrict__ codes,
-                                                                 const uint8_t *__restrict__ scales, int64_t rows,
-                                                                 int64_t cols, void *__restrict__ out) {
+                                                                 const uint8_t *__restrict__ scales, int64_t first,
+                                                                 int64_t rows, int64_t cols, void *__restrict__ out) {
   const int64_t kp = (cols + kQ4Pad - 1) / kQ4Pad * kQ4Pad;
   const int64_t r16 = (rows + kQ4ScaleRow - 1) / kQ4ScaleRow * kQ4ScaleRow;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + (threadIdx.x & 31) * 8;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 5);
+  const int64_t r0 = first + static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 5);
   if (c >= cols) return;
   uint32_t w[4];
   int byte[4];
@@ -315,12 +381,16 @@ hipError_t launch_q4_quantize(const Q4Batch &b, hipStream_t st) {
 
 hipError_t launch_q4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                 int32_t dt, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>((rows + 31) / 32), static_cast<uint32_t>((cols + 255) / 256));
-  if (dt == kF32)
-    hipLaunchKernelGGL(q4_dequantise_kernel<true>, grid, dim3(kThreads), 0, st, codes, scales, rows, cols, out);
-  else
-    hipLaunchKernelGGL(q4_dequantise_kernel<false>, grid, dim3(kThreads), 0, st, codes, scales, rows, cols, out);
-  return hipGetLastError();
+  for (int64_t first = 0; first < rows; first += kLaunchRows) {
+    const dim3 grid(static_cast<uint32_t>((std::min(rows - first, kLaunchRows) + 31) / 32), static_cast<uint32_t>((cols + 255) / 256));
+    if (dt == kF32)
+      hipLaunchKernelGGL(q4_dequantise_kernel<true>, grid, dim3(kThreads), 0, st, codes, scales, first, rows, cols, out);
+    else
+      hipLaunchKernelGGL(q4_dequantise_kernel<false>, grid, dim3(kThreads), 0, st, codes, scales, first, rows, cols, out);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace dmuon
