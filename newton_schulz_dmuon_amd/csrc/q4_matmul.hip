@@ -84,8 +84,12 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
   // the scales of a stage, 16 bytes a lane: [block][16 NN outputs], then [block]
   // [16 NT rows]
   const int sl = lane < 8 * NN ? lane : lane - 8 * NN;
+  // both tables' addresses are read here: chosen by lane as they stand in p, they
+  // come by a vector load, which the first stages' loads wait for
+  const uint8_t *sb0 = p.sb, *sa0 = p.sa;
+  asm volatile("" : "+s"(sb0), "+s"(sa0));
   const uint8_t *const scale0 =
-      lane < 8 * NN ? p.sb + sl / NN * rb + min(n0 + sl % NN * 16, rb - 16) : p.sa + sl / NT * ra + min(t0 + sl % NT * 16, ra - 16);
+      lane < 8 * NN ? sb0 + sl / NN * rb + min(n0 + sl % NN * 16, rb - 16) : sa0 + sl / NT * ra + min(t0 + sl % NT * 16, ra - 16);
   const int64_t scale_step = (lane < 8 * NN ? rb : ra) * (kQ4Pad / kQ4Block);
   f32x4 acc[NN][NT];
 #pragma unroll
