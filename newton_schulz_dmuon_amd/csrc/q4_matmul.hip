@@ -525,15 +525,28 @@ struct Plan {
   TileSplit split;
 };
 
+// Waves of a streaming work-group: one block of 16 x 16 is shared by eight where the
+// sum is long enough for each to take two blocks of codes.
+int stream_waves(int64_t kp, int nt, int nn) { return nt * nn == 1 && kp >= 16 * kQ4Pad ? 8 : 4; }
+
+// The weight's time from memory at 4.9 TB/s, in microseconds.
+float memory_us(int64_t outs, int64_t kp) { return static_cast<float>(outs * kp) * 0.53f / 4.9e6f; }
+
 // The streaming kernel's time in microseconds: a work-group takes in its weight's
 // and rows' codes at 53 GB/s, 256 of them at a time, while the weight comes from
-// memory at 4.9 TB/s; a quarter of the shorter of the two does not hide.
+// memory; a quarter of the shorter of the two does not hide.  Beside them the launch,
+// the waves' sums, and where LDS does not hold all work-groups at once the first
+// loads' latency of the rest (100 rows of 16384 x 256, 4 x 4: 512 work-groups in two
+// rounds 8.9 us, tiles 5.4).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
-  const float bytes = static_cast<float>((16 * nn + (rows <= 8 && nt == 1 ? 8 : 16 * nt)) * kp) * 0.53f;
-  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
-  const float memory = static_cast<float>(outs * kp) * 0.53f / 4.9e6f;
-  return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
+  const int xr = rows <= 8 && nt == 1 ? 8 : 16, waves = stream_waves(kp, nt, nn);
+  const int64_t slots = 256 * (160 * 1024 / (waves * stream_ahead(nt, nn, waves) * stream_stage(nt, nn, xr)));
+  const float sums = 0.2f + 0.09f * static_cast<float>(nt * nn);
+  const float bytes = static_cast<float>((16 * nn + nt * xr) * kp) * 0.53f;
+  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f, memory = memory_us(outs, kp);
+  return 2.f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
+         static_cast<float>((groups - 1) / slots) * (1.f + sums);
 }
 // Rows up to which it is considered.
 constexpr int64_t kStreamRows = 1024;
@@ -543,6 +556,7 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t kp) {
   if (rows == 0 || kp == 0) return pl;
   float us;
   pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
+  us += 0.35f * memory_us(outs, kp);  // of which the steps hide the rest
   if (rows <= kStreamRows) {
     for (const int nt : {1, 2, 4})
       for (const int nn : {1, 2, 4}) {
@@ -554,7 +568,7 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t kp) {
         pl.nn = nn;
       }
     if (pl.nt) {
-      pl.waves = pl.nt * pl.nn == 1 && kp >= 16 * kQ4Pad ? 8 : 4;
+      pl.waves = stream_waves(kp, pl.nt, pl.nn);
       pl.split = TileSplit{};
     }
   }

@@ -21,12 +21,14 @@ namespace dmuon {
 
 namespace {
 
-// Rows as the kernels read them: ld elements apart, a multiple of the kernel's step,
-// zeros behind the last.
+// Rows as the kernels read them: ld elements, a multiple of 8, zeros behind the
+// last.  The LDS-bound loads take 16-byte chunks; those of a row's last block that
+// lie behind its end come from kZeros.
 struct Rows {
   const uint8_t *x;
   int64_t ld;
 };
+__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 // ---- few rows: the weight's bytes ----
 //
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
   const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * 16;
-  const int nkb = static_cast<int>(p.kp / kQ4Pad);
+  const int nkb = static_cast<int>(p.kp / kQ4Pad), chunks = static_cast<int>(x.ld / 8);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
   lds_char *const ring = (lds_char *)smem + wave * (kAhead * kStage);
@@ -97,8 +99,16 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
     for (int i = 0; i < NN; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) piece(bb + ob[i][h], i * 2048 + h * 1024);
+    if (kb == nkb - 1 && chunks % 32 != 0) {
 #pragma unroll
-    for (int h = 0; h < XR / 2; ++h) piece(ba + oa[h], kRows + h * 1024);
+      for (int h = 0; h < XR / 2; ++h) {
+        const int chunk = kb * 32 + ((lane & 31) ^ ((2 * h + (lane >> 5)) & 15));
+        piece(chunk < chunks ? ba + oa[h] : (const uint8_t *)kZeros, kRows + h * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < XR / 2; ++h) piece(ba + oa[h], kRows + h * 1024);
+    }
     if (lane < 8 * NN) piece(scale0 + static_cast<int64_t>(kb) * (kQ4Pad / kQ4Block) * rb, kScales);
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -203,6 +213,7 @@ __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Produc
   const int wm = wave >> 2, wn = wave & 3;
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
+  const int chunks = static_cast<int>(x.ld / 8);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
 
   const uint8_t *const gb = p.b + n0 * kpb, *const ga = x.x + t0 * ldb;
@@ -239,15 +250,26 @@ __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Produc
     // opaque: the offsets are rebuilt at every issue instead of being kept
     // live across the loop
     asm volatile("" : "+v"(bt));
+    const uint8_t *const at = ga + static_cast<int64_t>(ks) * kRowBytes;
+    auto each_load = [&](auto go) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < TB / 64; ++j) {
-        // row s of the tile's LDS rows: quarter s / (TB / 4), then block and column
-        const int s = h * (TB / 2) + j * 32, in_quarter = s % (TB / 4);
-        const int row = s / (TB / 4) * (TB / 4) + in_quarter / 16;
-        load(ga + static_cast<int64_t>(ks) * kRowBytes, min(bt + row, lim_t), ldb, st + s * kRowBytes);
-      }
+        for (int j = 0; j < TB / 64; ++j) {
+          // row s of the tile's LDS rows: quarter s / (TB / 4), then block and column
+          const int s = h * (TB / 2) + j * 32, in_quarter = s % (TB / 4);
+          go(min(bt + s / (TB / 4) * (TB / 4) + in_quarter / 16, lim_t), st + s * kRowBytes);
+        }
+    };
+    if ((ks + 1) * 8 > chunks) {
+      const bool in = ks * 8 + static_cast<int>(chunk / 16) < chunks;
+      each_load([&](int row, lds_char *to) {
+        const uint8_t *const src = at + (__umul24(static_cast<uint32_t>(row), ldb) + chunk);
+        piece(in ? src : (const uint8_t *)kZeros, to + wn * 1024);
+      });
+    } else {
+      each_load([&](int row, lds_char *to) { load(at, row, ldb, to); });
+    }
   };
 
 #pragma unroll
@@ -256,7 +278,7 @@ __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Produc
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int first = kbeg * kStageSteps;
-  const int end = min(kend * kStageSteps, static_cast<int>(x.ld / kStep));
+  const int end = min(kend * kStageSteps, (chunks + 7) / 8);
 #pragma unroll
   for (int j = 0; j < kStageSteps; ++j) issue_weight(kbeg, j);
   issue_rows(first & 1, first);
@@ -374,7 +396,8 @@ void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
   const TileWork w = tile_work(sp, blockIdx.x, static_cast<uint32_t>(p.kp / kQ4Pad));
   const int64_t n0 = static_cast<int64_t>(w.a) * TA, t0 = static_cast<int64_t>(w.b) * TB;
   const int begin = w.begin * (kQ4Pad / kMidStep);
-  const int end = min(w.end * (kQ4Pad / kMidStep), static_cast<int>(x.ld / kMidStep));
+  const int chunks = static_cast<int>(x.ld / 8);
+  const int end = min(w.end * (kQ4Pad / kMidStep), (chunks + 15) / 16);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
   const int lim_n = static_cast<int>(min(p.outs - 1 - n0, static_cast<int64_t>(TA - 1)));
@@ -402,9 +425,18 @@ void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
   };
   auto issue_rows = [&](int ks) {
     lds_char *const st = lds + static_cast<uint32_t>(ks) % kRowStages * kRows;
-    const int64_t k = min(ks, end - 1);
+    const int k = min(ks, end - 1);
+    const uint8_t *const at = ga + static_cast<int64_t>(k) * (kMidStep * 2);
+    if ((k + 1) * 16 > chunks) {
 #pragma unroll
-    for (int j = 0; j < kRowLoads; ++j) piece(ga + k * (kMidStep * 2) + oa[j], st + (wave + 8 * j) * 1024);
+      for (int j = 0; j < kRowLoads; ++j) {
+        const int chunk = k * 16 + ((lane & 15) ^ ((4 * (wave + 8 * j) + (lane >> 4)) & 15));
+        piece(chunk < chunks ? at + oa[j] : (const uint8_t *)kZeros, st + (wave + 8 * j) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRowLoads; ++j) piece(at + oa[j], st + (wave + 8 * j) * 1024);
+    }
   };
   auto issue_weight = [&](int ks) {
     lds_char *const st = lds_w + static_cast<uint32_t>(ks) % kWeightStages * kWeight;
@@ -515,8 +547,9 @@ void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
 constexpr std::initializer_list<TileCost> kCosts = {
     {256, 256, 1, 4.6f, 5.9f}, {128, 256, 1, 3.2f, 3.5f}, {128, 128, 1, 1.75f, 2.1f}, {128, 64, 1, 0.97f, 1.15f}};
 
-// How a product runs: streamed (output blocks of a work-group) or in tiles; its rows' distance; and the bytes of its workspace's two
-// parts, the padded rows and the pieces' results.
+// How a product runs: streamed (output blocks of a work-group) or in tiles; its
+// rows' distance; and the bytes of its workspace's two parts, the padded rows and
+// the pieces' results.
 struct Plan {
   int nn;  // 0: tiles
   TileSplit split;
@@ -527,15 +560,23 @@ struct Plan {
 // Rows that a streaming work-group loads.
 int64_t stream_rows(int64_t rows) { return rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : 2; }
 
+// The weight's time from memory at 4.9 TB/s, in microseconds.
+float memory_us(int64_t outs, int64_t kp) { return static_cast<float>(outs * kp) * 0.53f / 4.9e6f; }
+
 // The streaming kernel's time in microseconds: a work-group takes in its weight's
-// codes and its rows at 53 GB/s, 256 of them at a time, while the weight comes from
-// memory at 4.9 TB/s; a quarter of the shorter of the two does not hide.
+// codes and its rows at 62 GB/s, 256 of them at a time, while the weight comes from
+// memory; a quarter of the shorter of the two does not hide.  Beside them the launch
+// and, where LDS does not hold all work-groups at once, the first loads' latency of
+// the rest (512 rows of 2048 x 1024, 64 outputs each: 1024 work-groups in four rounds
+// 13.3 us, tiles 8.7).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nn) {
   const int64_t groups = (rows + 15) / 16 * ((outs + 16 * nn - 1) / (16 * nn));
-  const float bytes = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(stream_rows(rows)));
-  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f;
-  const float memory = static_cast<float>(outs * kp) * 0.53f / 4.9e6f;
-  return 2.f + std::max(taken, memory) + 0.25f * std::min(taken, memory);
+  const int xr = static_cast<int>(stream_rows(rows));
+  const int64_t slots = 256 * (160 * 1024 / (kStreamWaves * stream_ahead(nn, xr) * stream_stage(nn, xr)));
+  const float bytes = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(xr));
+  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 62e3f, memory = memory_us(outs, kp);
+  return 2.3f + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
+         static_cast<float>((groups - 1) / slots) * 2.2f;
 }
 // Rows up to which it is considered.
 constexpr int64_t kStreamRows = 1024;
@@ -546,6 +587,7 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t inner) {
   const int64_t kp = (inner + kQ4Pad - 1) / kQ4Pad * kQ4Pad;
   float us;
   pl.split = choose_split(outs, rows, kp / kQ4Pad, kCosts, &us);
+  us += 0.35f * memory_us(outs, kp);  // of which the steps hide the rest
   if (rows <= kStreamRows) {
     for (const int nn : {1, 2, 4}) {
       const float s = stream_us(rows, outs, kp, nn);
@@ -556,8 +598,7 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t inner) {
     if (pl.nn) pl.split = TileSplit{};
   }
   // PLAN_HOOK
-  const int64_t step = pl.nn ? kQ4Pad : pl.split.tb == 256 ? kStep : kMidStep;
-  pl.ld = (inner + step - 1) / step * step;
+  pl.ld = (inner + 7) / 8 * 8;
   if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
   pl.piece_bytes = pl.split.ws_bytes();
   return pl;

@@ -344,7 +344,7 @@ EVERY_KERNEL = [(10, 33, 1117), (1, 17, 1408), (9, 5, 6797), (1, 30, 4703), (17,
                 (1671, 4760, 1199), (6738, 2463, 3873), (4, 20, 1813), (5, 40, 1118), (3, 4108, 1278), (6, 4720, 1383),
                 (9, 10357, 1144), (1, 13032, 1134), (4, 9356, 1472), (5, 9980, 1598), (9283, 4, 6531), (638, 6649, 1798),
                 (3720, 1543, 1202), (10351, 2, 13646), (724, 11302, 1331), (2637, 30, 1245), (12, 1, 13681),
-                (2326, 882, 1510), (6785, 131, 19804), (1208, 13114, 1424)]
+                (2326, 882, 1510), (6785, 131, 19804), (1208, 13114, 1424), (1, 4706, 5292)]
 
 
 @pytest.mark.parametrize("t,n,k", EVERY_KERNEL)
@@ -369,6 +369,36 @@ def test_every_kernel(t, n, k):
         b = torch.randn(t, n, device="cuda").to(dtype)
         want_b, mag_b = (want + b.double()).cpu().numpy(), (mag + b.double().abs()).cpu().numpy()
         check_sum(nsd.q4_weight_grad(d4, z4, base=b), want_b, mag_b, adds(k), (t, n, k, dtype, "onto a base"))
+
+
+# rows of whole 16-byte chunks that end inside a kernel's step, for every kernel that
+# multiplies bf16 rows
+CHUNK_SIZES = [(10, 33, 1128), (1, 17, 1416), (4, 20, 1816), (5, 40, 1128), (17, 2180, 1256), (1, 5006, 1512), (3, 4108, 1288),
+               (6, 4720, 1384), (9, 10357, 1144), (1, 13032, 1144), (4, 9356, 1480), (5, 9980, 1608), (10174, 136, 1168),
+               (9283, 4, 6536), (638, 6649, 1800), (3720, 1543, 1208), (10351, 2, 13656), (724, 11302, 1336),
+               (2637, 30, 1256), (12, 1, 13688), (2326, 882, 1512), (1671, 4760, 1208), (6785, 131, 19816),
+               (1208, 13114, 1432), (3, 50, 8), (70, 90, 24), (300, 300, 72), (130, 70, 136), (33, 40, 248)]
+
+
+@pytest.mark.parametrize("t,n,k", CHUNK_SIZES)
+def test_rows_of_whole_chunks(t, n, k):
+    """No workspace holds a copy of them; nothing of the next row, here NaN, reaches a
+    row's sums."""
+    print(f"rows of whole chunks {t} {n} {k}", flush=True)
+    torch.manual_seed(t + n)
+    x = torch.randn(t + 1, k, device="cuda").to(BF16)
+    x[1::2] = float("nan")
+    x[t] = float("nan")
+    x = x[:t]
+    w = (0.02 * torch.randn(n, k, device="cuda")).to(BF16)
+    w4 = nsd.q4_quantize_weights([w])[0]
+    wv = unpacked(w4.codes, w4.scales, n, k).t().contiguous()
+    rows = x[::2].double()
+    want, mag = (rows @ wv).cpu().numpy(), (rows.abs() @ wv.abs()).cpu().numpy()
+    for dtype in (BF16, F32):
+        got = nsd.q4_matmul(x, w4, dtype=dtype)
+        assert got[1::2].isnan().all()
+        check_sum(got[::2].contiguous(), want, mag, k + 25, (t, n, k, dtype))
 
 
 def test_no_rows():

@@ -210,11 +210,12 @@ def test_inputs_may_be_dropped_after_a_call():
 
 def test_a_captured_workspace_outlives_a_larger_call():
     """Captured with a warmed Workspace, which a larger product then uses eagerly:
-    the graph's scratch goes to no new tensor, and its replays stay right."""
+    the graph's scratch (rows of 1001 elements are copied there) goes to no new
+    tensor, and its replays stay right."""
     print("captured workspace", flush=True)
     rng = np.random.default_rng(5)
-    w = nsd.q4_quantize_weights([values(rng, 700, 1000, BF16, 0.02).cuda()])[0]
-    small, large = values(rng, 300, 1000, BF16).cuda(), values(rng, 5000, 1000, BF16).cuda()
+    w = nsd.q4_quantize_weights([values(rng, 700, 1001, BF16, 0.02).cuda()])[0]
+    small, large = values(rng, 300, 1001, BF16).cuda(), values(rng, 5000, 1001, BF16).cuda()
     want, want_large = nsd.q4_matmul(small, w), nsd.q4_matmul(large, w)
     ws = nsd.Workspace()
     nsd.q4_matmul(small, w, workspace=ws)

@@ -178,3 +178,13 @@ def test_tracked_inputs_are_refused(call):
 def test_a_parameter_may_be_quantised():
     with pytest.raises(nsd.DmuonError, match="GPU"):
         nsd.q4_quantize_weights([torch.nn.Parameter(torch.zeros(128, 256))])
+
+
+def test_rows_of_whole_chunks_need_no_copy(lib):
+    """A workspace holds a padded copy of bf16 rows only where 16-byte chunks do not
+    make up a row."""
+    out = ctypes.c_size_t(7)
+    for k in (8, 24, 72, 1000, 1416):
+        assert lib.dmuon_q4_rows_matmul_workspace_bytes(4, 256, k, ctypes.byref(out)) == _lib.OK and out.value == 0
+        assert lib.dmuon_q4_rows_matmul_workspace_bytes(4, 256, k + 1, ctypes.byref(out)) == _lib.OK
+        assert out.value == (4 * (k + 8) * 2 + 255) // 256 * 256
