@@ -572,7 +572,6 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t kp) {
       pl.split = TileSplit{};
     }
   }
-  // PLAN_HOOK
   return pl;
 }
 

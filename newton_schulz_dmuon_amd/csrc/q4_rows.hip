@@ -597,7 +597,6 @@ Plan make_plan(int64_t rows, int64_t outs, int64_t inner) {
     }
     if (pl.nn) pl.split = TileSplit{};
   }
-  // PLAN_HOOK
   pl.ld = (inner + 7) / 8 * 8;
   if (pl.ld != inner) pl.pad_bytes = (static_cast<size_t>(rows * pl.ld * 2) + 255) & ~static_cast<size_t>(255);
   pl.piece_bytes = pl.split.ws_bytes();
