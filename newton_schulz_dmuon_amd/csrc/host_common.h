@@ -34,9 +34,9 @@ struct Interval {
 int check_aliasing(std::vector<Interval> &iv);
 
 // Limits of the block products' entry points.  A launch takes fewer than 2^32
-// threads along its grid.  With these limits the
-// products' grids stay below that: at most 2^22 tiles of 128, or with 2^37
-// outputs 2^21 whole and as many ragged tiles of 256, of 512 threads each.
+// threads along its grid.  With these limits the products' grids stay below that: at
+// most 2^22 tiles of 128, or with 2^37 outputs 2^21 whole and as many ragged tiles of
+// 256, of 512 threads each.
 constexpr int64_t kMaxRows = int64_t(1) << 29;
 constexpr int64_t kMaxSide = int64_t(1) << 22;
 constexpr int64_t kMaxElems = int64_t(1) << 37;

@@ -8,7 +8,7 @@ namespace dmuon {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// 16 codes' words as a matrix operand: 4-bit operands take the first four.
+// A lane's 32 codes as a matrix operand: 4-bit operands take the first four words.
 __device__ __forceinline__ i32x8 codes_operand(const u32x4 &w) {
   return i32x8{static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w), 0, 0, 0, 0};
 }
@@ -57,6 +57,31 @@ __device__ __forceinline__ void exchange_halves(f32x4 (&acc)[FM][FN], int half, 
       const f32x4 got = *(const lds_f32x4 *)(other + (i * (FN / 2) + j) * 1024 + at);
       acc[i][j] = half == 0 ? acc[i][j] + got : got + acc[i][j + FN / 2];
     }
+}
+
+// R runs of N elements of base, `step` apart, `left` > 0 of which exist from the
+// first on (zeros behind them), a run's or all loads before the first use.  The kernels add
+// base before their first store: a load may not pass a store, since base may be out,
+// and each run would wait for its own.
+template <int N, int R>
+__device__ __forceinline__ void load_base(const void *base, int32_t dt, int64_t at, int step, int64_t left, float (&v)[R][N]) {
+  if (left >= (R - 1) * step + N) {
+    load_runs<N, R>(base, dt, at, step, v);
+    return;
+  }
+  // run by run, element by element
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    uint32_t w[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t i = at + min(static_cast<int64_t>(r * step + k), left - 1);
+      w[k] = dt == kF32 ? ((const g_u32 *)base)[i] : static_cast<uint32_t>(((const g_u16 *)base)[i]) << 16;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[r][k] = r * step + k < left ? __uint_as_float(w[k]) : 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 }  // namespace dmuon

@@ -44,6 +44,14 @@ __device__ __forceinline__ void each(F f) {
 // outputs; of up to eight rows, XR = 8, eight are loaded.  Rows and outputs behind
 // the last are clamped for the loads and not stored.  Column r of row block j is
 // row r * NT + j, so that a lane's NT scale bytes are one LDS word.
+//
+// Bound by the weight's bytes (one row by 14336 x 4096, 31 MB, 8.6 us out of HBM, 7.9
+// out of the memory-side cache: 3.6 TB/s with the launch, 2 us of it, 4.7 without),
+// from about 24 rows on by what a CU takes in (64 rows 10.8 us, 64 of 4096 x 14336
+// 12.5).  Wider work-groups read the rows' codes less often and have fewer waves a CU:
+// of 100 rows by 8192 x 8192 4 x 4 takes 14.0 us, 4 x 2 20.5, the tiles below 18.8; of
+// 64 by 4096 x 14336 2 x 2 12.5, 4 x 4 21.6, tiles 17.3.  2 x 1 and 4 x 1 were never
+// the best by more than 2%.
 constexpr int stream_stage(int nt, int nn, int xr) { return nn * 2048 + nt * xr * 128 + (nn + nt) * 128; }
 // Blocks in flight a wave.
 constexpr int stream_ahead(int nt, int nn, int waves) { return waves == 8 || nt * nn > 2 ? 2 : 3; }
@@ -171,6 +179,17 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
       read(u);
       multiply();
     }
+  constexpr int kRuns = (NN * NT + WAVES - 1) / WAVES;
+  float b[kRuns][1][4];
+#pragma unroll
+  for (int q = 0; q < kRuns; ++q) {
+    const int at = q * WAVES + wave;
+    const int64_t t = t0 + r16 * NT + at % NT, n = n0 + at / NT * 16 + 4 * g4;
+    if (p.base && at < NN * NT && t < p.rows && n < p.outs)
+      load_base<4, 1>(p.base, p.out_dt, t * p.outs + n, 0, p.outs - n, b[q]);
+    else
+      b[q][0][0] = b[q][0][1] = b[q][0][2] = b[q][0][3] = 0.f;
+  }
   // the waves' sums, each in its own part of the ring
   auto part = [&](int w, int b) { return (lds_f32x4 *)((lds_char *)smem + w * (kAhead * kStage) + b * 1024 + lane * 16); };
   static_assert(NN * NT * 1024 <= kAhead * kStage);
@@ -180,16 +199,18 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
     for (int j = 0; j < NT; ++j) *part(wave, i * NT + j) = acc[i][j];
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < (NN * NT + WAVES - 1) / WAVES; ++q) {
-    const int b = q * WAVES + wave;
-    if (b >= NN * NT) return;
-    f32x4 sum = *part(0, b);
+  for (int q = 0; q < kRuns; ++q) {
+    const int at = q * WAVES + wave;
+    if (at >= NN * NT) return;
+    f32x4 sum = *part(0, at);
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += *part(w, b);
-    const int64_t t = t0 + r16 * NT + b % NT, n = n0 + b / NT * 16 + 4 * g4;
+    for (int w = 1; w < WAVES; ++w) sum += *part(w, at);
+    const int64_t t = t0 + r16 * NT + at % NT, n = n0 + at / NT * 16 + 4 * g4;
     if (t >= p.rows) continue;
-    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    finish_run<4>(p.base, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = p.base ? b[q][0][k] + sum[k] : sum[k];
+    finish_run<4>(nullptr, p.out, p.out_dt, t * p.outs + n, p.outs - n, v);
   }
 }
 
@@ -204,6 +225,13 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
 // them.  The two halves of the work-group (wm) run in ping-pong: one half's waves
 // read fragments and issue the next stage's loads while the other half's multiply,
 // switching at every barrier.
+//
+// Bound by the power that the matrix instructions draw: 256 x 256 takes 1.28 us a step
+// on zero codes and 1.65 to 1.9 on random ones, where a loop of nothing else reaches
+// 7.1 PFLOP/s on random codes and 9.6 on zeros.  8192 rows by 14336 x 4096: 239 us, 4.0
+// PFLOP/s (a library product of the same type 350), of which the stores are 13%.  With
+// four waves of 128 x 128 it took 293 us for 290, with the next tile's first loads sent
+// before the stores 296 for 295: neither was kept.
 //
 // The order of rows in LDS is free, since every lane of a load picks its global
 // row, and is chosen for the ends of the pipeline: a wave's block i, row q holds
@@ -347,6 +375,22 @@ void q4_tile_kernel(Q4Product p, TileSplit sp) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 2, wn = wave & 3, r16 = lane & 15, g4 = lane >> 4;
   const TileOut o = tile_out(w, TA, TB, p.base, p.out, p.out_dt, p.rows, p.outs, p.ws);
+  // a tile of whole columns; at a ragged edge the runs, of which some end, wait each
+  // for its own
+  const bool base_first = o.base && o.cols >= TA;
+  if (base_first) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int r = wn * (TB / 4) + r16 * FN + j;
+      if (r >= o.rows) continue;
+      float b[4][FM];
+      load_runs<FM, 4>(o.base, o.dt, o.at + r * o.ld + wm * (TA / 2) + g4 * FM, 4 * FM, b);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[i][j][v] += b[v][i];
+    }
+  }
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int r = wn * (TB / 4) + r16 * FN + j;
@@ -357,7 +401,7 @@ void q4_tile_kernel(Q4Product p, TileSplit sp) {
       float run[FM];
 #pragma unroll
       for (int i = 0; i < FM; ++i) run[i] = acc[i][j][v];
-      finish_run<FM>(o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
+      finish_run<FM>(base_first ? nullptr : o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
   }
 }
@@ -368,9 +412,12 @@ void q4_tile_kernel(Q4Product p, TileSplit sp) {
 // which the latency of a step bounds.  Eight waves: 2 x 2 parts of 64 x TB / 2, and
 // two halves of a step's 256 codes, whose sums are added at the end (one wave for
 // all codes and half the part would read half as much again from LDS).  A ring of
-// four stages: a step waits for its own stage, loaded three steps ago, meets the
+// four stages (six of 64 rows): a step waits for its own stage, loaded three steps ago, meets the
 // other waves once, loads the stage that all of them have left and multiplies.  The
-// two waves of a SIMD hide each other's reads.
+// two waves of a SIMD hide each other's reads.  A step of 128 x 128 takes 0.44 us so;
+// with two stages and ping-pong 0.75, with whole steps a wave 0.59.  128 rows by 14336
+// x 4096: 13.3 us (128 x 128 16.2, streamed 16.7), 256: 16.6 (128 x 64 23.6, 128 x 256
+// 24.7).
 //
 // A lane's four rows of a weight block (q = 4 g4 + v) and FM blocks are consecutive
 // outputs: block i, row q holds output q * FM + i of the wave's part, block j,
@@ -486,10 +533,20 @@ void q4_mid_kernel(Q4Product p, TileSplit sp) {
   // every wave has read its last stage, and the loads that the last steps repeated
   // have landed
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  const TileOut o = tile_out(w, TA, TB, p.base, p.out, p.out_dt, p.rows, p.outs, p.ws);
+  // base comes while the halves are added
+  float b[FN / 2][2][8];
+  if (o.base) {
+#pragma unroll
+    for (int j = 0; j < FN / 2; ++j) {
+      const int r = wn * (16 * FN) + r16 * FN + half * (FN / 2) + j, c = wm * (16 * FM) + g4 * (4 * FM);
+      if (r >= o.rows || c >= o.cols) continue;
+      load_base<8, 2>(o.base, o.dt, o.at + r * o.ld + c, 8, o.cols - c, b[j]);
+    }
+  }
   constexpr int kSlot = FM * FN / 2 * 1024;
   static_assert(8 * kSlot <= kMidStages * kStage);
   exchange_halves<FM, FN>(acc, half, lds + wave * kSlot, lds + (wave ^ 4) * kSlot);
-  const TileOut o = tile_out(w, TA, TB, p.base, p.out, p.out_dt, p.rows, p.outs, p.ws);
 #pragma unroll
   for (int j = 0; j < FN / 2; ++j) {
     const int r = wn * (16 * FN) + r16 * FN + half * (FN / 2) + j;
@@ -500,8 +557,11 @@ void q4_mid_kernel(Q4Product p, TileSplit sp) {
       const int c = wm * (16 * FM) + g4 * (4 * FM) + h * 8;
       float run[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) run[e] = acc[(h * 8 + e) % FM][j][(h * 8 + e) / FM];
-      finish_run<8>(o.base, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
+      for (int e = 0; e < 8; ++e) {
+        run[e] = acc[(h * 8 + e) % FM][j][(h * 8 + e) / FM];
+        if (o.base) run[e] += b[j][h][e];
+      }
+      finish_run<8>(nullptr, o.out, o.dt, o.at + r * o.ld + c, o.cols - c, run);
     }
   }
 }
@@ -515,6 +575,8 @@ __global__ __launch_bounds__(256) void q4_empty_kernel(Q4Product p) {
   }
 }
 
+// A step's time in microseconds with few work-groups on the chip and with all, from
+// the slopes of times over the length of the sum.
 constexpr std::initializer_list<TileCost> kCosts = {
     {256, 256, 1, 1.2f, 1.85f}, {128, 256, 1, 0.85f, 1.04f}, {128, 128, 1, 0.44f, 0.58f}, {128, 64, 1, 0.34f, 0.4f}};
 
@@ -548,7 +610,8 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   return 2.f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
          static_cast<float>((groups - 1) / slots) * (1.f + sums);
 }
-// Rows up to which it is considered.
+// Rows up to which it is considered: 1000 of 1000 x 1000 5.6 us, tiles 6.3; 2000 of
+// 1024 x 1024 are 6.7 in tiles.
 constexpr int64_t kStreamRows = 1024;
 
 Plan make_plan(int64_t rows, int64_t outs, int64_t kp) {

@@ -42,6 +42,11 @@ __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
 // rows XR are loaded.  Rows and outputs behind the last are clamped for the loads
 // and not stored.
 //
+// Bound by the weight's bytes (one row by 14336 x 4096 8.8 us out of HBM, 8.2 out of
+// the memory-side cache), with more than a few rows by what a CU takes in (16 rows
+// 10.0 us, 16 of 4096 x 14336 13.5).  Two row blocks a work-group, and eight waves,
+// were no faster.
+//
 // A lane's 32 codes of a chunk (one block of the format) are multiplied eight an
 // instruction.
 constexpr int kStreamWaves = 4;
@@ -192,6 +197,11 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
 // step's rows and a quarter of the next stage of the weight.  The two halves of the
 // work-group (wm) run in ping-pong: one half's waves read fragments and issue loads
 // while the other half's expand and multiply, switching at every barrier.
+//
+// Bound by the matrix instructions at the clock that their power leaves: 2048 rows by
+// 14336 x 4096 176 to 180 us, 1.34 to 1.37 PFLOP/s, a large library product's rate
+// (1.36).  Expansions placed between the matrix instructions by hand changed nothing
+// (128 x 256: 65 -> 70 us of 2048 rows by 4096 x 4096).
 //
 // A lane's 16 codes of a step are k = 16 g4 + 0 .. 15, eight of them an instruction.
 // The order of rows in LDS is that of the 4-bit product's tiles.
@@ -375,6 +385,14 @@ void q4_rows_tile_kernel(Q4Product p, Rows x, TileSplit sp) {
 // stage, their 16-byte chunks XORed with (output / 4) mod 4, a row's elements 256
 // bytes, their chunks XORed with the row.
 //
+// A step of 256 elements takes 1.75 us for 128 x 128 (2.0 with one ring of three
+// stages, 2.5 with two and ping-pong) and 0.97 for 128 x 64: about half the matrix
+// instructions' alone (0.56 for 128 x 64, expansions 0.03 more), the rest what LDS
+// takes in and gives out between barriers.  64 x 64 parts with the sum shared by four
+// waves, which read 44% less from LDS, and reads and loads spread between the matrix
+// instructions were no faster (64 rows by 14336 x 4096 in these tiles 22.5 us, so
+// 24.3 and 25.0).
+//
 // Block i, row q of a wave's weight part holds output q * FM + i, block j, column r
 // of its rows row r * FN + j.
 constexpr int kMidThreads = 512, kMidStep = 128;
@@ -544,6 +562,8 @@ void q4_rows_mid_kernel(Q4Product p, Rows x, TileSplit sp) {
   }
 }
 
+// A step's time in microseconds with few work-groups on the chip and with all, from
+// the slopes of times over the length of the sum.
 constexpr std::initializer_list<TileCost> kCosts = {
     {256, 256, 1, 4.6f, 5.9f}, {128, 256, 1, 3.2f, 3.5f}, {128, 128, 1, 1.75f, 2.1f}, {128, 64, 1, 0.97f, 1.15f}};
 
@@ -578,7 +598,8 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nn) {
   return 2.3f + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
          static_cast<float>((groups - 1) / slots) * 2.2f;
 }
-// Rows up to which it is considered.
+// Rows up to which it is considered: 512 of 512 x 512 3.8 us, tiles 6.2; 1000 of 1000
+// x 1000 13.4, tiles 9.4.
 constexpr int64_t kStreamRows = 1024;
 
 Plan make_plan(int64_t rows, int64_t outs, int64_t inner) {
