@@ -34,6 +34,16 @@ __device__ __forceinline__ bf16x8 q4_expand8(uint32_t w, float s) {
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+// The streaming kernels' outputs tile of a work-group: a line of a scale table holds
+// 128 outputs' bytes of a block, so the 8 / NN work-groups that share it are eight
+// apart, on one XCD and its L2 (work-groups go to the XCDs in turn).
+template <int NN>
+__device__ __forceinline__ uint32_t line_tile(uint32_t n, uint32_t count) {
+  constexpr uint32_t kShare = 8 / NN, kChunk = 8 * kShare;
+  const uint32_t first = n / kChunk * kChunk, q = n - first;
+  return first + kChunk <= count ? first + q % 8 * kShare + q / 8 : n;
+}
+
 // Adds the sums of two waves that share a tile and split k: wave `half` 0 keeps the
 // rows' blocks j < FN / 2, half 1 the others, and each gets the other's part of its
 // own through LDS (slot: 1 KB times FM FN / 2 of each of the pair's waves).  The

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x - tb * nt) * (16 * NN), t0 = static_cast<int64_t>(tb) * 16;
+  const int64_t n0 = static_cast<int64_t>(line_tile<NN>(blockIdx.x - tb * nt, nt)) * (16 * NN), t0 = static_cast<int64_t>(tb) * 16;
   const int nkb = static_cast<int>(p.kp / kQ4Pad), chunks = static_cast<int>(x.ld / 8);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
