@@ -36,7 +36,8 @@ __device__ __forceinline__ bf16x8 q4_expand8(uint32_t w, float s) {
 
 // The streaming kernels' outputs tile of a work-group: a line of a scale table holds
 // 128 outputs' bytes of a block, so the 8 / NN work-groups that share it are eight
-// apart, on one XCD and its L2 (work-groups go to the XCDs in turn).
+// apart, on one XCD and its L2 (work-groups go to the XCDs in turn): one row by 4096 x
+// 14336 8.1 us, in the grid's order 9.3, of which every XCD read most of the table.
 template <int NN>
 __device__ __forceinline__ uint32_t line_tile(uint32_t n, uint32_t count) {
   constexpr uint32_t kShare = 8 / NN, kChunk = 8 * kShare;

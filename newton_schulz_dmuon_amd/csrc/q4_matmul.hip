@@ -45,8 +45,8 @@ __device__ __forceinline__ void each(F f) {
 // the last are clamped for the loads and not stored.  Column r of row block j is
 // row r * NT + j, so that a lane's NT scale bytes are one LDS word.
 //
-// Bound by the weight's bytes (one row by 14336 x 4096, 31 MB, 8.6 us out of HBM, 7.9
-// out of the memory-side cache: 3.6 TB/s with the launch, 2 us of it, 4.7 without),
+// Bound by the weight's bytes (one row by 14336 x 4096, 31 MB, 8.2 us out of HBM, 7.2
+// out of the memory-side cache: 3.8 TB/s with the launch, 2 us of it, 5.0 without),
 // from about 24 rows on by what a CU takes in (64 rows 10.8 us, 64 of 4096 x 14336
 // 12.5).  Wider work-groups read the rows' codes less often and have fewer waves a CU:
 // of 100 rows by 8192 x 8192 4 x 4 takes 14.0 us, 4 x 2 20.5, the tiles below 18.8; of
@@ -597,18 +597,20 @@ float memory_us(int64_t outs, int64_t kp) { return static_cast<float>(outs * kp)
 // The streaming kernel's time in microseconds: a work-group takes in its weight's
 // and rows' codes at 53 GB/s, 256 of them at a time, while the weight comes from
 // memory; a quarter of the shorter of the two does not hide.  Beside them the launch,
-// the waves' sums, and where LDS does not hold all work-groups at once the first
-// loads' latency of the rest (100 rows of 16384 x 256, 4 x 4: 512 work-groups in two
-// rounds 8.9 us, tiles 5.4).
+// the waves' sums, the start of more work-groups than CUs, and where LDS does not hold
+// all of them at once the first loads' latency of the rest, which the others of a CU
+// hide (100 rows of 16384 x 256, 4 x 4: 512 work-groups in two rounds, one a CU, 8.9
+// us, tiles 5.4; one row of 18944 x 3584, 1 x 1: 1184 in two rounds, four a CU, 8.9,
+// tiles 11.1).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const int64_t groups = (rows + 16 * nt - 1) / (16 * nt) * ((outs + 16 * nn - 1) / (16 * nn));
   const int xr = rows <= 8 && nt == 1 ? 8 : 16, waves = stream_waves(kp, nt, nn);
-  const int64_t slots = 256 * (160 * 1024 / (waves * stream_ahead(nt, nn, waves) * stream_stage(nt, nn, xr)));
+  const int64_t resident = 160 * 1024 / (waves * stream_ahead(nt, nn, waves) * stream_stage(nt, nn, xr));  // a CU
   const float sums = 0.2f + 0.09f * static_cast<float>(nt * nn);
-  const float bytes = static_cast<float>((16 * nn + nt * xr) * kp) * 0.53f;
-  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 53e3f, memory = memory_us(outs, kp);
-  return 2.f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
-         static_cast<float>((groups - 1) / slots) * (1.f + sums);
+  const float bytes = static_cast<float>((16 * nn + nt * xr) * kp) * 0.53f, turns = static_cast<float>((groups + 255) / 256);
+  const float taken = turns * bytes / 53e3f, memory = memory_us(outs, kp);
+  return 1.5f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) + 0.3f * (turns - 1.f) +
+         static_cast<float>((groups - 1) / (256 * resident)) * (1.f + sums) / static_cast<float>(resident);
 }
 // Rows up to which it is considered: 1000 of 1000 x 1000 5.6 us, tiles 6.3; 2000 of
 // 1024 x 1024 are 6.7 in tiles.

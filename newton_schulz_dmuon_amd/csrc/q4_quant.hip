@@ -13,7 +13,7 @@
 //
 // Bound by memory: 8192 x 4096 bf16 in both forms reads 67 and writes 36 MB in 24.8
 // us (4.1 TB/s; a large copy 5.0), fp32 40 us, a list of matrices of 218 M elements
-// 164 us (4.1 TB/s).  Rounding by random bytes is bound by the vector ALUs (busy 97%
+// 164 us (4.1 TB/s).  Rounding by random bytes is bound by the vector ALUs (busy 87%
 // of the time): 41 us in both forms, 28 in one.  One row 3.9 us, a launch's latency.
 
 #include <algorithm>

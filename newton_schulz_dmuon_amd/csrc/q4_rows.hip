@@ -42,9 +42,9 @@ __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
 // rows XR are loaded.  Rows and outputs behind the last are clamped for the loads
 // and not stored.
 //
-// Bound by the weight's bytes (one row by 14336 x 4096 8.8 us out of HBM, 8.2 out of
+// Bound by the weight's bytes (one row by 14336 x 4096 8.7 us out of HBM, 7.8 out of
 // the memory-side cache), with more than a few rows by what a CU takes in (16 rows
-// 10.0 us, 16 of 4096 x 14336 13.5).  Two row blocks a work-group, and eight waves,
+// 10.0 us, 16 of 4096 x 14336 13.1).  Two row blocks a work-group, and eight waves,
 // were no faster.
 //
 // A lane's 32 codes of a chunk (one block of the format) are multiplied eight an
@@ -585,18 +585,21 @@ float memory_us(int64_t outs, int64_t kp) { return static_cast<float>(outs * kp)
 
 // The streaming kernel's time in microseconds: a work-group takes in its weight's
 // codes and its rows at 62 GB/s, 256 of them at a time, while the weight comes from
-// memory; a quarter of the shorter of the two does not hide.  Beside them the launch
-// and, where LDS does not hold all work-groups at once, the first loads' latency of
-// the rest (512 rows of 2048 x 1024, 64 outputs each: 1024 work-groups in four rounds
-// 13.3 us, tiles 8.7).
+// memory; a quarter of the shorter of the two does not hide.  Beside them the launch,
+// of several turns the last work-groups' end and, where LDS does not hold all
+// work-groups at once, the first loads' latency of the rest, which the others of a CU
+// hide (512 rows of 2048 x 1024, 64 outputs each: 1024 work-groups in four rounds, one
+// a CU, 13.3 us, tiles 8.7; one row of 18944 x 3584, 16 outputs each: 1184 in two
+// rounds, four a CU, 9.7, 64 outputs each 11.5).
 float stream_us(int64_t rows, int64_t outs, int64_t kp, int nn) {
   const int64_t groups = (rows + 15) / 16 * ((outs + 16 * nn - 1) / (16 * nn));
   const int xr = static_cast<int>(stream_rows(rows));
-  const int64_t slots = 256 * (160 * 1024 / (kStreamWaves * stream_ahead(nn, xr) * stream_stage(nn, xr)));
-  const float bytes = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(xr));
-  const float taken = static_cast<float>((groups + 255) / 256) * bytes / 62e3f, memory = memory_us(outs, kp);
-  return 2.3f + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
-         static_cast<float>((groups - 1) / slots) * 2.2f;
+  const int64_t resident = 160 * 1024 / (kStreamWaves * stream_ahead(nn, xr) * stream_stage(nn, xr));  // a CU
+  const float work = static_cast<float>(kp) * (16 * nn * 0.53f + 2.f * static_cast<float>(xr)) / 62e3f;
+  const int64_t turns = (groups + 255) / 256;
+  const float taken = static_cast<float>(turns) * work, memory = memory_us(outs, kp);
+  return 1.8f + std::max(taken, memory) + 0.25f * std::min(taken, memory) + (turns > 1 ? 0.3f * work : 0.f) +
+         static_cast<float>((groups - 1) / (256 * resident)) * 2.2f / static_cast<float>(resident);
 }
 // Rows up to which it is considered: 512 of 512 x 512 3.8 us, tiles 6.2; 1000 of 1000
 // x 1000 13.4, tiles 9.4.
