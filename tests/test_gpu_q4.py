@@ -813,3 +813,34 @@ def test_binding_refusals():
     assert status(nsd.q4_weight_grad, d4, x4, out=buf[:128 * 256].view(128, 256),
                   base=buf[64:].view(128, 256)) == _lib.ERR_ALIAS
     torch.cuda.synchronize()
+
+
+def test_a_matrix_against_itself():
+    print("a matrix against itself", flush=True)
+    torch.manual_seed(4)
+    for t, k in ((5, 64), (130, 300), (700, 1000)):
+        x = torch.randn(t, k, device="cuda").to(BF16)
+        x4 = nsd.q4_quantize(x, transposed=True)
+        v, c = unpacked(x4.codes, x4.scales, t, k), unpacked(x4.codes_t, x4.scales_t, k, t)
+        for dtype in (BF16, F32):
+            check_sum(nsd.q4_matmul(x4, x4, dtype=dtype), (v @ v.t()).cpu().numpy(), (v.abs() @ v.abs().t()).cpu().numpy(),
+                      adds(k), (t, k, dtype))
+            check_sum(nsd.q4_weight_grad(x4, x4, dtype=dtype), (c @ c.t()).cpu().numpy(), (c.abs() @ c.abs().t()).cpu().numpy(),
+                      adds(t), (t, k, dtype, "weight gradient"))
+
+
+def test_more_rows_than_a_launch_reads_back():
+    """2^28 rows are read back a launch."""
+    rows = (1 << 28) + 77
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("not enough memory")
+    print("rows of two launches", flush=True)
+    q = nsd.Q4Matrix.empty(rows, 1, "cuda", True, False)
+    q.codes.zero_()
+    q.scales.fill_(127)
+    q.codes[:, 0] = 2  # the code of 1
+    q.codes[-100:, 0] = 4  # of 2
+    got = nsd.q4_dequantize(q)
+    assert (got[:-100] == 1).all() and (got[-100:] == 2).all()
+    del q, got
+    torch.cuda.empty_cache()
