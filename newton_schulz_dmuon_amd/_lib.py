@@ -206,8 +206,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
                  "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
                  "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad",
-            "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
-            "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul"):
+                 "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
+                 "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.dmuon_abi_version() != ABI_VERSION:
         raise ImportError(f"libdmuon ABI {lib.dmuon_abi_version()} != {ABI_VERSION}")

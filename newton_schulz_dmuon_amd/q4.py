@@ -33,12 +33,13 @@ gives the same bits.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import List, Optional, Sequence
 
 from . import _lib
-from ._lib import DmuonError, Q4SourceDesc, load
+from ._lib import DmuonError, Q4SourceDesc, check, load
 from .api import Workspace, _allocating, _dtype_code, _ptr
-from .q8 import _check_stream, _check_tensor, _check_untracked, _invalid, _keep, _matrix, _run, _up, _workspace
+from .q8 import _check_stream, _check_tensor, _check_untracked, _invalid, _keep, _matrix, _run, _scratch, _up
 
 BLOCK = 32
 PAD = 256
@@ -77,9 +78,26 @@ class Q4Matrix:
         return sum(t.numel() for t in self.tensors() if t is not None)
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(call: str, rows: int, outs: int, inner: int) -> int:
+    """A function of the sizes alone."""
+    need = ctypes.c_size_t(0)
+    check(getattr(load(), call + "_workspace_bytes")(rows, outs, inner, ctypes.byref(need)))
+    return need.value
+
+
+_uint8 = None
+
+
 def _check_form(codes, scales, rows: int, cols: int, what: str, device) -> None:
-    import torch
+    global _uint8
     cp = _up(cols, PAD)
+    if (codes.shape == (rows, cp // 2) and scales.shape == (cp // BLOCK, _up(rows, 16)) and
+            codes.dtype is _uint8 and scales.dtype is _uint8 and codes.device == device and scales.device == device and
+            codes.is_contiguous() and scales.is_contiguous()):
+        return
+    import torch
+    _uint8 = torch.uint8  # at first None, which no type is
     _check_tensor(codes, f"{what}'s codes", (rows, cp // 2), torch.uint8, device)
     _check_tensor(scales, f"{what}'s scales", (cp // BLOCK, _up(rows, 16)), torch.uint8, device)
 
@@ -249,14 +267,15 @@ def q4_matmul(a, w: Q4Matrix, transpose: bool = False, out=None, dtype=None,
     dt = _dtype_code(out)
     lib = load()
     if isinstance(a, Q4Matrix):
-        ws, nws, keep = _workspace(lib.dmuon_q4_matmul_workspace_bytes, (rows, outs, inner), workspace, device, stream)
+        need = _workspace_bytes("dmuon_q4_matmul", rows, outs, inner)
+        ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a_codes, a_scales, codes, scales))
         _run(lib.dmuon_q4_matmul, device, stream, a_codes.data_ptr(), a_scales.data_ptr(), rows, codes.data_ptr(),
              scales.data_ptr(), outs, inner, None, out.data_ptr(), dt, ws, nws)
     else:
-        ws, nws, keep = _workspace(lib.dmuon_q4_rows_matmul_workspace_bytes, (rows, outs, inner), workspace, device,
-                                   stream)
+        need = _workspace_bytes("dmuon_q4_rows_matmul", rows, outs, inner)
+        ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a, codes, scales))
         _run(lib.dmuon_q4_rows_matmul, device, stream, a.data_ptr(), rows, codes.data_ptr(), scales.data_ptr(), outs,
@@ -290,7 +309,7 @@ def q4_weight_grad(dy: Q4Matrix, x: Q4Matrix, out=None, dtype=None, base=None,
         _check_tensor(base, "base", (rows, outs), out.dtype, device)
     dt = _dtype_code(out)
     lib = load()
-    ws, nws, keep = _workspace(lib.dmuon_q4_matmul_workspace_bytes, (rows, outs, tokens), workspace, device, stream)
+    ws, nws, keep = _scratch(_workspace_bytes("dmuon_q4_matmul", rows, outs, tokens), workspace, device, stream)
     if stream is not None:
         _keep(device, stream, (out,), made, (codes, scales, x_codes, x_scales, base))
     _run(lib.dmuon_q4_matmul, device, stream, codes.data_ptr(), scales.data_ptr(), rows, x_codes.data_ptr(),

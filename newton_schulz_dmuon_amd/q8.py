@@ -144,7 +144,6 @@ def _matrix(t, what: str):
 def _run(fn, device, stream, *args) -> None:
     """One C call on ``stream`` (by default ``device``'s current one), with
     ``device`` current, since kernels are loaded per device."""
-    import torch
     index = device.index
     if stream is None:
         handle = _raw_stream(index)
@@ -153,6 +152,7 @@ def _run(fn, device, stream, *args) -> None:
     if _current_device() == index:
         status = fn(*args, handle)
     else:
+        import torch
         with torch.cuda.device(device):
             status = fn(*args, handle)
     if status:
@@ -255,14 +255,19 @@ def _workspace(call, sizes, workspace: Optional[Workspace], device, stream):
     the tensor keeps the memory until the launches are enqueued."""
     need = ctypes.c_size_t(0)
     check(call(*sizes, ctypes.byref(need)))
-    if need.value == 0:
+    return _scratch(need.value, workspace, device, stream)
+
+
+def _scratch(need: int, workspace: Optional[Workspace], device, stream):
+    """``_workspace`` of ``need`` bytes."""
+    if need == 0:
         return None, 0, None
     if workspace is not None:
-        buf = workspace.get(need.value, device, stream)
+        buf = workspace.get(need, device, stream)
     else:
         import torch
         with _allocating(stream):
-            buf = torch.empty(need.value, dtype=torch.uint8, device=device)
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
     return buf.data_ptr(), buf.numel(), buf
 
 
