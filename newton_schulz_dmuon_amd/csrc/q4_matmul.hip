@@ -67,7 +67,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
-  const int64_t n0 = static_cast<int64_t>(line_tile<NN>(blockIdx.x - tb * nt, nt)) * (16 * NN), t0 = static_cast<int64_t>(tb) * (16 * NT);
+  const int64_t n0 = static_cast<int64_t>(line_tile<NN>(blockIdx.x - tb * nt, nt)) * (16 * NN);
+  const int64_t t0 = static_cast<int64_t>(tb) * (16 * NT);
   const int nkb = static_cast<int>(p.kp / kQ4Pad);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2);
   const int64_t ra = (p.rows + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
@@ -97,7 +98,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
   const uint8_t *sb0 = p.sb, *sa0 = p.sa;
   asm volatile("" : "+s"(sb0), "+s"(sa0));
   const uint8_t *const scale0 =
-      lane < 8 * NN ? sb0 + sl / NN * rb + min(n0 + sl % NN * 16, rb - 16) : sa0 + sl / NT * ra + min(t0 + sl % NT * 16, ra - 16);
+      lane < 8 * NN ? sb0 + sl / NN * rb + min(n0 + sl % NN * 16, rb - 16)
+                    : sa0 + sl / NT * ra + min(t0 + sl % NT * 16, ra - 16);
   const int64_t scale_step = (lane < 8 * NN ? rb : ra) * (kQ4Pad / kQ4Block);
   f32x4 acc[NN][NT];
 #pragma unroll
@@ -316,7 +318,8 @@ __device__ __forceinline__ void q4_tile(lds_char *const lds, const Q4Product &p,
   auto read = [&](const lds_char *op, int i, int sub) {
     return *(const lds_u32x4 *)(op + (sub ? at0 ^ 64 : at0) + i * (16 * kRowBytes));
   };
-  const uint32_t at_b = static_cast<uint32_t>(kScaleA + wm * (TA / 2 * kStepBlocks) + g4 * (TA / 2) + ((r16 & 3) * 4 + (r16 >> 2)) * FM);
+  const uint32_t at_b = static_cast<uint32_t>(kScaleA + wm * (TA / 2 * kStepBlocks) + g4 * (TA / 2) +
+                                              ((r16 & 3) * 4 + (r16 >> 2)) * FM);
   const uint32_t at_a = static_cast<uint32_t>(kScaleB + g4 * TB + wn * (TB / 4) + r16 * FN);
 
   issue(kbeg & 1, kbeg);
@@ -462,8 +465,9 @@ void q4_mid_kernel(Q4Product p, TileSplit sp) {
   const uint8_t *const gb = p.b + n0 * kpb, *const ga = static_cast<const uint8_t *>(p.a) + t0 * kpb;
   // scales, 16 bytes a lane: the weight's [block][output], then the rows'
   const int s16 = wave * kScaleLanes + lane, s_rows = s16 - TA / 2;
-  const uint8_t *const gs = s16 < TA / 2 ? p.sb + s16 / (TA / 16) * rb + min(n0 + s16 % (TA / 16) * 16, rb - 16)
-                                         : p.sa + s_rows / (TB / 16) % kStepBlocks * ra + min(t0 + s_rows % (TB / 16) * 16, ra - 16);
+  const uint8_t *const gs =
+      s16 < TA / 2 ? p.sb + s16 / (TA / 16) * rb + min(n0 + s16 % (TA / 16) * 16, rb - 16)
+                   : p.sa + s_rows / (TB / 16) % kStepBlocks * ra + min(t0 + s_rows % (TB / 16) * 16, ra - 16);
   const int64_t gs_step = (s16 < TA / 2 ? rb : ra) * kStepBlocks;
   auto issue = [&](int kb) {
     lds_char *const st = lds + static_cast<uint32_t>(kb) % kMidStages * kStage;
@@ -692,7 +696,8 @@ hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
     return hipGetLastError();
   }
   const Plan pl = plan_of(p.rows, p.outs, p.kp);
-  if (pl.nt == 1) return pl.nn == 2 ? launch_stream<2, 4>(p, st) : pl.waves == 8 ? launch_stream<1, 8>(p, st) : launch_stream<1, 4>(p, st);
+  if (pl.nt == 1 && pl.nn == 2) return launch_stream<2, 4>(p, st);
+  if (pl.nt == 1) return pl.waves == 8 ? launch_stream<1, 8>(p, st) : launch_stream<1, 4>(p, st);
   if (pl.nt == 2) return launch_stream<2, 2, 4, 16>(p, st);
   if (pl.nt == 4) return pl.nn == 2 ? launch_stream<4, 2, 4, 16>(p, st) : launch_stream<4, 4, 4, 16>(p, st);
   const TileSplit &sp = pl.split;

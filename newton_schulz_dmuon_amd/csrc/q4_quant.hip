@@ -14,9 +14,11 @@
 // Bound by memory: 8192 x 4096 bf16 in both forms reads 67 and writes 36 MB in 24.8
 // us (4.1 TB/s; a large copy 5.0), fp32 40 us, a list of matrices of 218 M elements
 // 164 us (4.1 TB/s).  Rounding by random bytes is bound by the vector ALUs (busy 87%
-// of the time): 41 us in both forms, 28 in one.  One row 3.9 us, a launch's latency.
+// of the time): 39 us in both forms (41 with the scale always in two factors), 28 in
+// one.  One row 3.9 us, a launch's latency.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "q4_internal.h"
 #include "q8_device.h"
@@ -114,10 +116,13 @@ template <bool F32> __device__ __forceinline__ uint32_t stride4_max(uint32_t v) 
 // a step between codes has 512, 1024 or 2048 (values below 2, 4 and 6), up iff what
 // lies above the code below is at least 255.5 - n of 256 parts.  Cutting a value to
 // whole units changes no comparison, since every threshold is a whole number of
-// them.  more * unit: 2^(10 - e), in two factors, of which fp32 holds each.
+// them.  more * unit: 2^(10 - e), in two factors where fp32 does not hold it.
+template <bool TINY>
 __device__ __forceinline__ u16x2 random_codes(float a, float b, float more, float unit, u16x2 n) {
-  const u16x2 u = {static_cast<unsigned short>(static_cast<uint32_t>(__builtin_fabsf(a) * more * unit)),
-                   static_cast<unsigned short>(static_cast<uint32_t>(__builtin_fabsf(b) * more * unit))};
+  const float x = TINY ? __builtin_fabsf(a) * more : __builtin_fabsf(a);
+  const float y = TINY ? __builtin_fabsf(b) * more : __builtin_fabsf(b);
+  const u16x2 u = {static_cast<unsigned short>(static_cast<uint32_t>(x * unit)),
+                   static_cast<unsigned short>(static_cast<uint32_t>(y * unit))};
   const u16x2 wide = __builtin_elementwise_min(u >> 11, u16x2{2, 2});
   return ((u + ((n + n + 1) << wide)) >> (wide + 9)) + (wide + wide);
 }
@@ -132,18 +137,19 @@ template <bool F32> struct Pairs {
 };
 
 // The codes of eight elements, the first in the lowest four bits.  n(k): the random
-// bytes of pair k, in the halves of a word.
-template <bool F32, bool RANDOM, typename N>
+// bytes of pair k, in the halves of a word.  Without TINY byte is at least kTinyByte.
+constexpr int kTinyByte = 10;
+template <bool F32, bool RANDOM, bool TINY, typename N>
 __device__ __forceinline__ uint32_t codes8(const Pairs<F32> &x, int byte, N n) {
   uint32_t w = 0;
   if constexpr (RANDOM) {
     const float unit = __uint_as_float(static_cast<uint32_t>(min(264 - byte, 254)) << 23);
-    const float more = __uint_as_float(static_cast<uint32_t>(127 + max(10 - byte, 0)) << 23);
+    const float more = __uint_as_float(static_cast<uint32_t>(127 + max(kTinyByte - byte, 0)) << 23);
     uint32_t two[4];  // a pair's two codes in the lowest byte
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t c = __builtin_bit_cast(
-          uint32_t, random_codes(x.get(2 * k), x.get(2 * k + 1), more, unit, __builtin_bit_cast(u16x2, n(k))));
+          uint32_t, random_codes<TINY>(x.get(2 * k), x.get(2 * k + 1), more, unit, __builtin_bit_cast(u16x2, n(k))));
       const uint32_t sign = F32 ? __builtin_amdgcn_perm(x.w[(2 * k + 1) % (F32 ? 8 : 4)], x.w[2 * k % (F32 ? 8 : 4)], 0x07060302u)
                                 : x.w[k];  // in bits 15 and 31
       const uint32_t s = (sign >> 12 & 0x00080008u) | c;
@@ -189,6 +195,16 @@ __device__ __forceinline__ void load_bytes(const uint8_t *p, int64_t at, int64_t
     const uint32_t shift = static_cast<uint32_t>(at + r * step) & 3;
     n[r] = u32x2{__builtin_amdgcn_alignbyte(lo[r].y, lo[r].x, shift), __builtin_amdgcn_alignbyte(hi[r], lo[r].y, shift)};
   }
+}
+
+// Whether rounding by random bytes takes its scale in two factors somewhere in the
+// wave.
+template <bool RANDOM> __device__ __forceinline__ bool any_tiny(const int (&b)[8]) {
+  if (!RANDOM) return false;
+  int least = b[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) least = min(least, b[k]);
+  return __builtin_amdgcn_ballot_w64(least < kTinyByte) != 0;
 }
 
 // Eight scale bytes as two words.
@@ -266,17 +282,23 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
     bytes[r] = scale_byte(F32 ? a : max(a << 16, a & 0xffff0000u));
   }
   if (codes) {
+    auto write_rows = [&](auto tiny) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      Pairs<F32> v;
+      for (int r = 0; r < 8; ++r) {
+        Pairs<F32> v;
 #pragma unroll
-      for (int k = 0; k < W; ++k) v.w[k] = x[r].w[k];
-      // bytes 2 k and 2 k + 1 of the row's
-      const uint32_t w = codes8<F32, RANDOM>(v, bytes[r], [&](int k) {
-        return __builtin_amdgcn_perm(0, n[r][k / 2], k % 2 ? 0x0c030c02u : 0x0c010c00u);
-      });
-      if (r0 + r < rows && c0 < kp) *(g_u32 *)(codes + (r0 + r) * (kp / 2) + c0 / 2) = w;
-    }
+        for (int k = 0; k < W; ++k) v.w[k] = x[r].w[k];
+        // bytes 2 k and 2 k + 1 of the row's
+        const uint32_t w = codes8<F32, RANDOM, tiny>(v, bytes[r], [&](int k) {
+          return __builtin_amdgcn_perm(0, n[r][k / 2], k % 2 ? 0x0c030c02u : 0x0c010c00u);
+        });
+        if (r0 + r < rows && c0 < kp) *(g_u32 *)(codes + (r0 + r) * (kp / 2) + c0 / 2) = w;
+      }
+    };
+    if (any_tiny<RANDOM>(bytes))
+      write_rows(std::true_type{});
+    else
+      write_rows(std::false_type{});
     if ((lane & 3) == 0 && r0 < r16 && c0 < kp) *(g_u32x2 *)(b.scales[mi] + c0 / kQ4Block * r16 + r0) = pack8(bytes);
   }
   if (!codes_t) return;
@@ -284,21 +306,29 @@ __device__ __forceinline__ void quantise_tile(const Q4Batch &b, int32_t mi, int6
 #pragma unroll
   for (int k = 0; k < W; ++k) col_max[k] = stride4_max<F32>(col_max[k]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 8; ++k)
     bytes[k] = scale_byte(F32 ? col_max[k % W] : k % 2 ? col_max[k / 2 % W] & 0xffff0000u : col_max[k / 2 % W] << 16);
-    Pairs<F32> v;
+  auto put_columns = [&](auto tiny) {
 #pragma unroll
-    for (int r = 0; r < W; ++r) {
-      if constexpr (F32)
-        v.w[r] = x[r].w[k];
-      else
-        v.w[r] = __builtin_amdgcn_perm(x[2 * r + 1].w[k / 2], x[2 * r].w[k / 2], k % 2 ? 0x07060302u : 0x05040100u);
+    for (int k = 0; k < 8; ++k) {
+      Pairs<F32> v;
+#pragma unroll
+      for (int r = 0; r < W; ++r) {
+        if constexpr (F32)
+          v.w[r] = x[r].w[k];
+        else
+          v.w[r] = __builtin_amdgcn_perm(x[2 * r + 1].w[k / 2], x[2 * r].w[k / 2], k % 2 ? 0x07060302u : 0x05040100u);
+      }
+      // byte k of two rows'
+      *(lds_u32 *)(lds + (cl + k) * kPitch + rl / 2) = codes8<F32, RANDOM, tiny>(v, bytes[k], [&](int q) {
+        return __builtin_amdgcn_perm(n[2 * q + 1][k / 4], n[2 * q][k / 4], 0x0c040c00u + (k % 4) * 0x00010001u);
+      });
     }
-    // byte k of two rows'
-    *(lds_u32 *)(lds + (cl + k) * kPitch + rl / 2) = codes8<F32, RANDOM>(v, bytes[k], [&](int q) {
-      return __builtin_amdgcn_perm(n[2 * q + 1][k / 4], n[2 * q][k / 4], 0x0c040c00u + (k % 4) * 0x00010001u);
-    });
-  }
+  };
+  if (any_tiny<RANDOM>(bytes))
+    put_columns(std::true_type{});
+  else
+    put_columns(std::false_type{});
   if ((lane & 12) == 0 && c0 < c16 && r0 < rp) *(g_u32x2 *)(b.scales_t[mi] + r0 / kQ4Block * c16 + c0) = pack8(bytes);
   __syncthreads();
 #pragma unroll
@@ -390,7 +420,8 @@ hipError_t launch_q4_quantize(const Q4Batch &b, hipStream_t st) {
 hipError_t launch_q4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                 int32_t dt, hipStream_t st) {
   for (int64_t first = 0; first < rows; first += kLaunchRows) {
-    const dim3 grid(static_cast<uint32_t>((std::min(rows - first, kLaunchRows) + 31) / 32), static_cast<uint32_t>((cols + 255) / 256));
+    const int64_t here = std::min(rows - first, kLaunchRows);
+    const dim3 grid(static_cast<uint32_t>((here + 31) / 32), static_cast<uint32_t>((cols + 255) / 256));
     if (dt == kF32)
       hipLaunchKernelGGL(q4_dequantise_kernel<true>, grid, dim3(kThreads), 0, st, codes, scales, first, rows, cols, out);
     else

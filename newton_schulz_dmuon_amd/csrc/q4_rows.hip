@@ -64,7 +64,8 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t nt = static_cast<uint32_t>((p.outs + 16 * NN - 1) / (16 * NN)), tb = uniform(blockIdx.x / nt);
-  const int64_t n0 = static_cast<int64_t>(line_tile<NN>(blockIdx.x - tb * nt, nt)) * (16 * NN), t0 = static_cast<int64_t>(tb) * 16;
+  const int64_t n0 = static_cast<int64_t>(line_tile<NN>(blockIdx.x - tb * nt, nt)) * (16 * NN);
+  const int64_t t0 = static_cast<int64_t>(tb) * 16;
   const int nkb = static_cast<int>(p.kp / kQ4Pad), chunks = static_cast<int>(x.ld / 8);
   const uint32_t kpb = static_cast<uint32_t>(p.kp / 2), ldb = static_cast<uint32_t>(x.ld * 2);
   const int64_t rb = (p.outs + kQ4ScaleRow - 1) & ~static_cast<int64_t>(kQ4ScaleRow - 1);
@@ -307,7 +308,8 @@ __device__ __forceinline__ void q4_rows_tile(lds_char *const lds, const Q4Produc
     u32x4 fa[FN][2];
     uint32_t sb[FM / 4];
     const int block = 2 * part + (g4 >> 1);
-    const lds_char *const ws = st + kScales + wm * (TA / 2 * kStageBlocks) + block * (TA / 2) + ((r16 & 3) * 4 + (r16 >> 2)) * FM;
+    const lds_char *const ws =
+        st + kScales + wm * (TA / 2 * kStageBlocks) + block * (TA / 2) + ((r16 & 3) * 4 + (r16 >> 2)) * FM;
     if constexpr (FM == 8) {
       const u32x2 w = *(const lds_u32x2 *)ws;
       sb[0] = w.x;

@@ -110,6 +110,23 @@ def test_quantise(t, k, dtype, by_bytes):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_random_bytes_at_the_smallest_scales(dtype):
+    """2^(10 - e) is more than fp32 holds for e below -117: blocks on both sides of
+    that, and zero ones, beside each other in both directions."""
+    print(f"smallest scales {dtype}", flush=True)
+    rng = np.random.default_rng(12)
+    for t, k in ((300, 520), (512, 512), (37, 1001)):
+        e = rng.integers(-132, -100, (-(-t // 40), -(-k // 24)))
+        e[rng.random(e.shape) < 0.1] = -1000
+        scale = np.exp2(e.astype(np.float64)).repeat(40, 0).repeat(24, 1)[:t, :k]
+        x = torch.from_numpy(rng.standard_normal((t, k)) * scale).to(dtype)
+        r = rng.integers(0, 256, (t, k)).astype(np.uint8)
+        q = nsd.q4_quantize(x.cuda(), transposed=True, random=torch.from_numpy(r).cuda())
+        torch.cuda.synchronize()
+        check_matrix(q, host(x), r)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("transposed", [True, False])
 def test_weights(dtype, transposed):
     print(f"weights {dtype} {transposed}", flush=True)
