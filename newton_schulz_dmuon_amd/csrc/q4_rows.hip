@@ -28,7 +28,7 @@ struct Rows {
   const uint8_t *x;
   int64_t ld;
 };
-__device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+__device__ const __attribute__((aligned(16))) uint32_t kZeros[4] = {0, 0, 0, 0};
 
 // ---- few rows: the weight's bytes ----
 //
