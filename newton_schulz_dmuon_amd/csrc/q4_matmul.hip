@@ -613,7 +613,8 @@ float stream_us(int64_t rows, int64_t outs, int64_t kp, int nt, int nn) {
   const float sums = 0.2f + 0.09f * static_cast<float>(nt * nn);
   const float bytes = static_cast<float>((16 * nn + nt * xr) * kp) * 0.53f, turns = static_cast<float>((groups + 255) / 256);
   const float taken = turns * bytes / 53e3f, memory = memory_us(outs, kp);
-  return 1.5f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) + 0.3f * (turns - 1.f) +
+  return 1.5f + sums + std::max(taken, memory) + 0.25f * std::min(taken, memory) +
+         0.1f * static_cast<float>(nt * nn) * (turns - 1.f) +
          static_cast<float>((groups - 1) / (256 * resident)) * (1.f + sums) / static_cast<float>(resident);
 }
 // Rows up to which it is considered: 1000 of 1000 x 1000 5.6 us, tiles 6.3; 2000 of
