@@ -545,6 +545,16 @@ int dmuon_q4_quantize(const dmuon_q4_source *m, int32_t n, void *stream);
 int dmuon_q4_dequantize(const void *codes, const void *scales, int64_t rows,
                         int64_t cols, void *out, int32_t dtype, void *stream);
 
+/* out[r][c] = src[r * row_step + c * col_step], r < rows, c < cols: codes or scales
+ * that lie otherwise than the format says (a transposed view, rows of a larger
+ * buffer), laid out for the other calls.  All are bytes; src has any alignment, out
+ * is 16-byte aligned.  rows = 0 or cols = 0 is a no-op.
+ * Errors: INVALID_ARG (rows or cols < 0 or > 2^29, cols no multiple of 16, more than
+ * 2^36 bytes, a step < 0, src over more than 2^47 bytes), MISALIGNED, ALIAS (out
+ * overlaps src's span), HIP. */
+int dmuon_q4_copy(const void *src, int64_t rows, int64_t cols, int64_t row_step,
+                  int64_t col_step, void *out, void *stream);
+
 /* Bytes of device workspace dmuon_q4_matmul needs for these sizes (0 for many).
  * Host-only. */
 int dmuon_q4_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner,

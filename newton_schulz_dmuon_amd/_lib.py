@@ -48,8 +48,9 @@ EXPORTED = ("dmuon_abi_version", "dmuon_error_string", "dmuon_last_error",
             "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
             "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
             "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad",
-            "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
-            "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul")
+            "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_copy",
+            "dmuon_q4_matmul_workspace_bytes", "dmuon_q4_matmul",
+            "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul")
 
 # DMUON_NOALLOC_SCRATCH_BYTES
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -195,6 +196,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                          vp]
     lib.dmuon_q4_quantize.argtypes = [P(Q4SourceDesc), c_i32, vp]
     lib.dmuon_q4_dequantize.argtypes = [vp, vp, c_i64, c_i64, vp, c_i32, vp]
+    lib.dmuon_q4_copy.argtypes = [vp, c_i64, c_i64, c_i64, c_i64, vp, vp]
     lib.dmuon_q4_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
     lib.dmuon_q4_matmul.argtypes = [vp, vp, c_i64, vp, vp, c_i64, c_i64, vp, vp, c_i32, vp, size_t, vp]
     lib.dmuon_q4_rows_matmul_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, P(size_t)]
@@ -206,8 +208,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "dmuon_chain_status_offset", "dmuon_q8_quantize", "dmuon_q8_quantize_weights",
                  "dmuon_q8_matmul_workspace_bytes", "dmuon_q8_matmul",
                  "dmuon_q8_weight_grad_workspace_bytes", "dmuon_q8_weight_grad",
-                 "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_matmul_workspace_bytes",
-                 "dmuon_q4_matmul", "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul"):
+                 "dmuon_q4_quantize", "dmuon_q4_dequantize", "dmuon_q4_copy",
+                 "dmuon_q4_matmul_workspace_bytes", "dmuon_q4_matmul",
+                 "dmuon_q4_rows_matmul_workspace_bytes", "dmuon_q4_rows_matmul"):
         getattr(lib, name).restype = ctypes.c_int
     if lib.dmuon_abi_version() != ABI_VERSION:
         raise ImportError(f"libdmuon ABI {lib.dmuon_abi_version()} != {ABI_VERSION}")

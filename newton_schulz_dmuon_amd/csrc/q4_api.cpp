@@ -141,6 +141,32 @@ int dmuon_q4_dequantize(const void *codes, const void *scales, int64_t rows, int
   });
 }
 
+int dmuon_q4_copy(const void *src, int64_t rows, int64_t cols, int64_t row_step, int64_t col_step, void *out,
+                  void *stream) {
+  return guarded([&]() -> int {
+    // at most 2^22 + 2^23 tiles of 128 x 128, whose threads stay below 2^32
+    if (rows < 0 || rows > kMaxRows) return fail(DMUON_ERR_INVALID_ARG, "rows %lld", (long long)rows);
+    if (cols < 0 || cols > kMaxRows || cols % kQ4ScaleRow != 0)
+      return fail(DMUON_ERR_INVALID_ARG, "columns %lld", (long long)cols);
+    if (too_large(rows, 2 * cols))
+      return fail(DMUON_ERR_INVALID_ARG, "%lld x %lld bytes exceed 2^36", (long long)rows, (long long)cols);
+    constexpr int64_t kMaxExtent = int64_t(1) << 47;
+    if (row_step < 0 || row_step > kMaxExtent || col_step < 0 || col_step > kMaxExtent)
+      return fail(DMUON_ERR_INVALID_ARG, "steps %lld, %lld", (long long)row_step, (long long)col_step);
+    if (rows == 0 || cols == 0) return DMUON_OK;
+    const __int128 extent = static_cast<__int128>(rows - 1) * row_step + static_cast<__int128>(cols - 1) * col_step + 1;
+    if (extent > kMaxExtent) return fail(DMUON_ERR_INVALID_ARG, "src spans more than 2^47 bytes");
+    Buffers b;
+    int rc;
+    if ((rc = b.add(src, static_cast<int64_t>(extent), false, "src", 1))) return rc;
+    if ((rc = b.add(out, rows * cols, true, "out"))) return rc;
+    if ((rc = b.check())) return rc;
+    return check_launch(launch_q4_copy(static_cast<const uint8_t *>(src), rows, cols, row_step, col_step,
+                                       static_cast<uint8_t *>(out), static_cast<hipStream_t>(stream)),
+                        "q4 copy launch");
+  });
+}
+
 int dmuon_q4_matmul_workspace_bytes(int64_t rows, int64_t outs, int64_t inner, size_t *out_bytes) {
   return guarded([&]() -> int {
     if (!out_bytes) return fail(DMUON_ERR_INVALID_ARG, "out_bytes is NULL");

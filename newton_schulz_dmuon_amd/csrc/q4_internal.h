@@ -42,6 +42,9 @@ hipError_t launch_q4_quantize(const Q4Batch &b, hipStream_t st);
 // The values of codes and scales, rows x cols.
 hipError_t launch_q4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *out,
                                 int32_t dt, hipStream_t st);
+// out[r][c] = src[r * row_step + c * col_step], bytes; cols is a multiple of 16.
+hipError_t launch_q4_copy(const uint8_t *src, int64_t rows, int64_t cols, int64_t row_step, int64_t col_step,
+                          uint8_t *out, hipStream_t st);
 
 // out[t][n] = base[t][n] + sum over blocks b of 2^(sa[b][t] + sb[b][n] - 254) *
 // sum over k in b of a[t][k] b[n][k]; all strides follow from the sizes.

@@ -401,6 +401,59 @@ __global__ __launch_bounds__(kThreads) void q4_dequantise_kernel(const uint8_t *
   }
 }
 
+// Codes and scales whose bytes lie apart, copied to where a product's loads find them:
+// out[r][c] = src[r * row_step + c * col_step].  128 x 128 bytes a work-group, in 4 x 4
+// patches turned in registers and, through LDS, written 16 bytes a lane.  With WORDS
+// the rows of a column are consecutive (a transposed view) and whole words are loaded,
+// otherwise bytes.
+constexpr int kCopyTile = 128, kCopyPitch = kCopyTile / 4 + 1;  // words of a row in LDS
+
+template <bool WORDS>
+__global__ __launch_bounds__(kThreads) void q4_copy_kernel(const uint8_t *__restrict__ src, int64_t rows, int64_t cols,
+                                                           int64_t row_step, int64_t col_step,
+                                                           uint8_t *__restrict__ out) {
+  __shared__ __align__(16) char smem[kCopyTile * kCopyPitch * 4];
+  lds_char *const lds = (lds_char *)smem;
+  const uint32_t across = static_cast<uint32_t>((cols + kCopyTile - 1) / kCopyTile);
+  const uint32_t ti = uniform(blockIdx.x / across), tj = uniform(blockIdx.x - ti * across);
+  const int64_t r0 = static_cast<int64_t>(ti) * kCopyTile, c0 = static_cast<int64_t>(tj) * kCopyTile;
+  const bool along_rows = row_step <= col_step;  // the direction of a wave's lanes
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = i * kThreads + static_cast<int>(threadIdx.x), fast = q & 31, slow = q >> 5;
+    const int pr = along_rows ? fast : slow, pc = along_rows ? slow : fast;
+    const int64_t r = r0 + 4 * pr;
+    uint32_t w[4];  // four rows' bytes of a column; behind the last row and column those of the last
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint8_t *const p = src + min(c0 + 4 * pc + k, cols - 1) * col_step;
+      if (WORDS && r + 4 <= rows) {
+        w[k] = *(const g_u32 *)(p + r);
+        continue;
+      }
+      w[k] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        w[k] |= static_cast<uint32_t>(((const g_u8 *)p)[min(r + b, rows - 1) * row_step]) << (8 * b);
+    }
+    const uint32_t lo01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), lo23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+    const uint32_t hi01 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u), hi23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    const uint32_t row[4] = {__builtin_amdgcn_perm(lo23, lo01, 0x05040100u), __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
+                             __builtin_amdgcn_perm(hi23, hi01, 0x05040100u), __builtin_amdgcn_perm(hi23, hi01, 0x07060302u)};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) *(lds_u32 *)(lds + ((4 * pr + b) * kCopyPitch + pc) * 4) = row[b];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = i * kThreads + static_cast<int>(threadIdx.x), r = q >> 3, c = (q & 7) * 16;
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = *(const lds_u32 *)(lds + r * kCopyPitch * 4 + c + 4 * k);
+    if (r0 + r < rows && c0 + c < cols) *(g_u32x4 *)(out + (r0 + r) * cols + c0 + c) = w;
+  }
+}
+
 int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
 }  // namespace
@@ -430,6 +483,17 @@ hipError_t launch_q4_dequantize(const uint8_t *codes, const uint8_t *scales, int
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+hipError_t launch_q4_copy(const uint8_t *src, int64_t rows, int64_t cols, int64_t row_step, int64_t col_step,
+                          uint8_t *out, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(up(rows, kCopyTile) / kCopyTile * (up(cols, kCopyTile) / kCopyTile)));
+  const bool words = row_step == 1 && col_step % 4 == 0 && reinterpret_cast<uintptr_t>(src) % 4 == 0;
+  if (words)
+    hipLaunchKernelGGL(q4_copy_kernel<true>, grid, dim3(kThreads), 0, st, src, rows, cols, row_step, col_step, out);
+  else
+    hipLaunchKernelGGL(q4_copy_kernel<false>, grid, dim3(kThreads), 0, st, src, rows, cols, row_step, col_step, out);
+  return hipGetLastError();
 }
 
 }  // namespace dmuon

@@ -38,7 +38,7 @@ from typing import List, Optional, Sequence
 
 from . import _lib
 from ._lib import DmuonError, Q4SourceDesc, check, load
-from .api import Workspace, _allocating, _dtype_code, _ptr
+from .api import Workspace, _allocating, _dtype_code, _mark_used, _ptr
 from .q8 import _check_stream, _check_tensor, _check_untracked, _invalid, _keep, _matrix, _run, _scratch, _up
 
 BLOCK = 32
@@ -58,7 +58,9 @@ class Q4Matrix:
     256 / 32, rows up to 16]`` (exponent + 127), for sums along its rows; and
     ``codes_t`` ``[cols, rows up to 256 / 2]`` with ``scales_t``, the same of its
     transpose.  Either form may be None, and dropped when no product needs it any
-    more."""
+    more.  Codes and scales that a call reads may have any strides and begin anywhere
+    (what is not contiguous, or begins at no multiple of 16 bytes, is copied first, on
+    the call's stream); those that one writes may not."""
 
     __slots__ = ("rows", "cols", "codes", "scales", "codes_t", "scales_t")
 
@@ -89,29 +91,56 @@ def _workspace_bytes(call: str, rows: int, outs: int, inner: int) -> int:
 _uint8 = None
 
 
-def _check_form(codes, scales, rows: int, cols: int, what: str, device) -> None:
+def _check_form(codes, scales, rows: int, cols: int, what: str, device, strided: bool = False) -> bool:
+    """Whether both are contiguous, which they have to be unless ``strided``."""
     global _uint8
     cp = _up(cols, PAD)
     if (codes.shape == (rows, cp // 2) and scales.shape == (cp // BLOCK, _up(rows, 16)) and
             codes.dtype is _uint8 and scales.dtype is _uint8 and codes.device == device and scales.device == device and
             codes.is_contiguous() and scales.is_contiguous()):
-        return
+        return True
     import torch
     _uint8 = torch.uint8  # at first None, which no type is
-    _check_tensor(codes, f"{what}'s codes", (rows, cp // 2), torch.uint8, device)
-    _check_tensor(scales, f"{what}'s scales", (cp // BLOCK, _up(rows, 16)), torch.uint8, device)
+    _check_tensor(codes, f"{what}'s codes", (rows, cp // 2), torch.uint8, device, not strided)
+    _check_tensor(scales, f"{what}'s scales", (cp // BLOCK, _up(rows, 16)), torch.uint8, device, not strided)
+    return codes.is_contiguous() and scales.is_contiguous()
+
+
+def _dense(t, stream):
+    """``t``, or a copy that is contiguous and aligned and belongs to the call's
+    stream."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    import torch
+    with _allocating(stream):
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if stream is not None:
+        _mark_used(stream, t)
+    _run(load().dmuon_q4_copy, t.device, stream, t.data_ptr(), *t.shape, *t.stride(), out.data_ptr())
+    return out
+
+
+def _dense_form(codes, scales, stream):
+    codes, scales = _dense(codes, stream), _dense(scales, stream)
+    return codes, scales, (codes.data_ptr(), scales.data_ptr())
 
 
 def _form_of(q: Q4Matrix, transposed: bool, what: str):
-    """The codes and scales of one form, its rows and its columns."""
+    """The codes and scales of one form, its rows and its columns, and their
+    addresses: None if they do not lie as the kernels read them, who then get
+    ``_dense_form``."""
     codes, scales = (q.codes_t, q.scales_t) if transposed else (q.codes, q.scales)
     if codes is None or scales is None:
         raise _invalid(f"{what} has no {'transposed ' if transposed else ''}codes")
     if not codes.is_cuda:
         raise _invalid(f"{what}'s codes are on {codes.device}, not on a GPU")
     rows, cols = (q.cols, q.rows) if transposed else (q.rows, q.cols)
-    _check_form(codes, scales, rows, cols, what, codes.device)
-    return codes, scales, rows, cols
+    at = None
+    if _check_form(codes, scales, rows, cols, what, codes.device, True):
+        at = codes.data_ptr(), scales.data_ptr()
+        if (at[0] | at[1]) & 15:
+            at = None
+    return codes, scales, rows, cols, at
 
 
 def _check_out(q: Q4Matrix, rows: int, cols: int, device) -> None:
@@ -225,17 +254,18 @@ def q4_dequantize(q: Q4Matrix, transpose: bool = False, out=None, dtype=None, st
     """The values of ``q``'s codes, ``[rows, cols]``, or of its transposed codes,
     ``[cols, rows]``: bf16 (the default) or fp32, both exact (``4 * 2^126``, which
     the types' largest values round to, becomes infinite)."""
-    codes, scales, rows, cols = _form_of(q, transpose, "q")
+    codes, scales, rows, cols, at = _form_of(q, transpose, "q")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
     out, made = _result(out, (rows, cols), dtype, device, stream)
     dt = _dtype_code(out)
+    if at is None:
+        codes, scales, at = _dense_form(codes, scales, stream)
     if stream is not None:
         _keep(device, stream, (out,), made, (codes, scales))
     if cols:
-        _run(load().dmuon_q4_dequantize, device, stream, codes.data_ptr(), scales.data_ptr(), rows, cols,
-             out.data_ptr(), dt)
+        _run(load().dmuon_q4_dequantize, device, stream, *at, rows, cols, out.data_ptr(), dt)
     return out
 
 
@@ -247,12 +277,12 @@ def q4_matmul(a, w: Q4Matrix, transpose: bool = False, out=None, dtype=None,
     leading dimensions are flattened.  ``out`` takes the result; its dtype is then
     the result's."""
     import torch
-    codes, scales, outs, inner = _form_of(w, transpose, "the weight")
+    codes, scales, outs, inner, at = _form_of(w, transpose, "the weight")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
     if isinstance(a, Q4Matrix):
-        a_codes, a_scales, rows, cols = _form_of(a, False, "a")
+        a_codes, a_scales, rows, cols, a_at = _form_of(a, False, "a")
         on = a_codes.device
     else:
         on, rows, cols = _matrix(a, "a")
@@ -266,20 +296,22 @@ def q4_matmul(a, w: Q4Matrix, transpose: bool = False, out=None, dtype=None,
     out, made = _result(out, (rows, outs), dtype, device, stream)
     dt = _dtype_code(out)
     lib = load()
+    if at is None:
+        codes, scales, at = _dense_form(codes, scales, stream)
     if isinstance(a, Q4Matrix):
+        if a_at is None:
+            a_codes, a_scales, a_at = _dense_form(a_codes, a_scales, stream)
         need = _workspace_bytes("dmuon_q4_matmul", rows, outs, inner)
         ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a_codes, a_scales, codes, scales))
-        _run(lib.dmuon_q4_matmul, device, stream, a_codes.data_ptr(), a_scales.data_ptr(), rows, codes.data_ptr(),
-             scales.data_ptr(), outs, inner, None, out.data_ptr(), dt, ws, nws)
+        _run(lib.dmuon_q4_matmul, device, stream, *a_at, rows, *at, outs, inner, None, out.data_ptr(), dt, ws, nws)
     else:
         need = _workspace_bytes("dmuon_q4_rows_matmul", rows, outs, inner)
         ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a, codes, scales))
-        _run(lib.dmuon_q4_rows_matmul, device, stream, a.data_ptr(), rows, codes.data_ptr(), scales.data_ptr(), outs,
-             inner, out.data_ptr(), dt, ws, nws)
+        _run(lib.dmuon_q4_rows_matmul, device, stream, a.data_ptr(), rows, *at, outs, inner, out.data_ptr(), dt, ws, nws)
     return out
 
 
@@ -291,8 +323,8 @@ def q4_weight_grad(dy: Q4Matrix, x: Q4Matrix, out=None, dtype=None, base=None,
     ``muon_step``) or a new tensor of ``dtype`` (``base``'s, or bf16).  ``base``
     has the result's dtype and may be ``out`` itself, which adds to the gradient
     in place."""
-    codes, scales, rows, tokens = _form_of(dy, True, "dy")
-    x_codes, x_scales, outs, x_tokens = _form_of(x, True, "x")
+    codes, scales, rows, tokens, at = _form_of(dy, True, "dy")
+    x_codes, x_scales, outs, x_tokens, x_at = _form_of(x, True, "x")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
@@ -309,9 +341,13 @@ def q4_weight_grad(dy: Q4Matrix, x: Q4Matrix, out=None, dtype=None, base=None,
         _check_tensor(base, "base", (rows, outs), out.dtype, device)
     dt = _dtype_code(out)
     lib = load()
+    if at is None:
+        codes, scales, at = _dense_form(codes, scales, stream)
+    if x_at is None:
+        x_codes, x_scales, x_at = _dense_form(x_codes, x_scales, stream)
     ws, nws, keep = _scratch(_workspace_bytes("dmuon_q4_matmul", rows, outs, tokens), workspace, device, stream)
     if stream is not None:
         _keep(device, stream, (out,), made, (codes, scales, x_codes, x_scales, base))
-    _run(lib.dmuon_q4_matmul, device, stream, codes.data_ptr(), scales.data_ptr(), rows, x_codes.data_ptr(),
-         x_scales.data_ptr(), outs, tokens, base.data_ptr() if base is not None else None, out.data_ptr(), dt, ws, nws)
+    _run(lib.dmuon_q4_matmul, device, stream, *at, rows, *x_at, outs, tokens,
+         base.data_ptr() if base is not None else None, out.data_ptr(), dt, ws, nws)
     return out

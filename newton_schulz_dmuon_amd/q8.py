@@ -99,7 +99,7 @@ def _invalid(message: str) -> DmuonError:
     return DmuonError(_lib.ERR_INVALID_ARG, message)
 
 
-def _check_tensor(t, what: str, shape, dtype, device) -> None:
+def _check_tensor(t, what: str, shape, dtype, device, contiguous: bool = True) -> None:
     """The checks that the C call cannot make: a kernel would read another
     device's memory, or past the end of a smaller tensor."""
     if t.device != device:
@@ -108,7 +108,7 @@ def _check_tensor(t, what: str, shape, dtype, device) -> None:
         raise DmuonError(_lib.ERR_UNSUPPORTED_DTYPE, f"{what} has dtype {t.dtype}, not {dtype}")
     if t.shape != shape:
         raise _invalid(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise _invalid(f"{what} must be contiguous")
 
 
