@@ -200,7 +200,7 @@ def _packed(x):
     a = 2 * q.abs()  # 0 1 2 3 4 6 8 12
     code = torch.where(a < 4, a, torch.where(a < 8, a / 2 + 2, a / 4 + 4)).to(torch.uint8) | (torch.signbit(q).to(torch.uint8) << 3)
     scales = torch.nn.functional.pad((e + 127).to(torch.uint8).t(), (0, _up(r, 16) - r), value=LO + 127).contiguous()
-    return {"codes": (code[:, 0::2] | (code[:, 1::2] << 4)).contiguous(), "scales": scales, "rows": r, "cols": c}
+    return {"codes": code[:, 0::2] | (code[:, 1::2] << 4), "scales": scales, "rows": r, "cols": c}
 
 
 def _unpacked(q):
