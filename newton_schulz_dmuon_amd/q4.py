@@ -122,7 +122,7 @@ def _dense(t, stream):
 
 def _dense_form(codes, scales, stream):
     codes, scales = _dense(codes, stream), _dense(scales, stream)
-    return codes, scales, (codes.data_ptr(), scales.data_ptr())
+    return codes, scales, codes.data_ptr(), scales.data_ptr()
 
 
 def _form_of(q: Q4Matrix, transposed: bool, what: str):
@@ -135,12 +135,11 @@ def _form_of(q: Q4Matrix, transposed: bool, what: str):
     if not codes.is_cuda:
         raise _invalid(f"{what}'s codes are on {codes.device}, not on a GPU")
     rows, cols = (q.cols, q.rows) if transposed else (q.rows, q.cols)
-    at = None
     if _check_form(codes, scales, rows, cols, what, codes.device, True):
-        at = codes.data_ptr(), scales.data_ptr()
-        if (at[0] | at[1]) & 15:
-            at = None
-    return codes, scales, rows, cols, at
+        p, ps = codes.data_ptr(), scales.data_ptr()
+        if not (p | ps) & 15:
+            return codes, scales, rows, cols, p, ps
+    return codes, scales, rows, cols, None, None
 
 
 def _check_out(q: Q4Matrix, rows: int, cols: int, device) -> None:
@@ -254,18 +253,18 @@ def q4_dequantize(q: Q4Matrix, transpose: bool = False, out=None, dtype=None, st
     """The values of ``q``'s codes, ``[rows, cols]``, or of its transposed codes,
     ``[cols, rows]``: bf16 (the default) or fp32, both exact (``4 * 2^126``, which
     the types' largest values round to, becomes infinite)."""
-    codes, scales, rows, cols, at = _form_of(q, transpose, "q")
+    codes, scales, rows, cols, p, ps = _form_of(q, transpose, "q")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
     out, made = _result(out, (rows, cols), dtype, device, stream)
     dt = _dtype_code(out)
-    if at is None:
-        codes, scales, at = _dense_form(codes, scales, stream)
+    if p is None:
+        codes, scales, p, ps = _dense_form(codes, scales, stream)
     if stream is not None:
         _keep(device, stream, (out,), made, (codes, scales))
     if cols:
-        _run(load().dmuon_q4_dequantize, device, stream, *at, rows, cols, out.data_ptr(), dt)
+        _run(load().dmuon_q4_dequantize, device, stream, p, ps, rows, cols, out.data_ptr(), dt)
     return out
 
 
@@ -277,12 +276,12 @@ def q4_matmul(a, w: Q4Matrix, transpose: bool = False, out=None, dtype=None,
     leading dimensions are flattened.  ``out`` takes the result; its dtype is then
     the result's."""
     import torch
-    codes, scales, outs, inner, at = _form_of(w, transpose, "the weight")
+    codes, scales, outs, inner, p, ps = _form_of(w, transpose, "the weight")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
     if isinstance(a, Q4Matrix):
-        a_codes, a_scales, rows, cols, a_at = _form_of(a, False, "a")
+        a_codes, a_scales, rows, cols, a_p, a_ps = _form_of(a, False, "a")
         on = a_codes.device
     else:
         on, rows, cols = _matrix(a, "a")
@@ -296,22 +295,22 @@ def q4_matmul(a, w: Q4Matrix, transpose: bool = False, out=None, dtype=None,
     out, made = _result(out, (rows, outs), dtype, device, stream)
     dt = _dtype_code(out)
     lib = load()
-    if at is None:
-        codes, scales, at = _dense_form(codes, scales, stream)
+    if p is None:
+        codes, scales, p, ps = _dense_form(codes, scales, stream)
     if isinstance(a, Q4Matrix):
-        if a_at is None:
-            a_codes, a_scales, a_at = _dense_form(a_codes, a_scales, stream)
+        if a_p is None:
+            a_codes, a_scales, a_p, a_ps = _dense_form(a_codes, a_scales, stream)
         need = _workspace_bytes("dmuon_q4_matmul", rows, outs, inner)
         ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a_codes, a_scales, codes, scales))
-        _run(lib.dmuon_q4_matmul, device, stream, *a_at, rows, *at, outs, inner, None, out.data_ptr(), dt, ws, nws)
+        _run(lib.dmuon_q4_matmul, device, stream, a_p, a_ps, rows, p, ps, outs, inner, None, out.data_ptr(), dt, ws, nws)
     else:
         need = _workspace_bytes("dmuon_q4_rows_matmul", rows, outs, inner)
         ws, nws, keep = _scratch(need, workspace, device, stream)
         if stream is not None:
             _keep(device, stream, (out,), made, (a, codes, scales))
-        _run(lib.dmuon_q4_rows_matmul, device, stream, a.data_ptr(), rows, *at, outs, inner, out.data_ptr(), dt, ws, nws)
+        _run(lib.dmuon_q4_rows_matmul, device, stream, a.data_ptr(), rows, p, ps, outs, inner, out.data_ptr(), dt, ws, nws)
     return out
 
 
@@ -323,8 +322,8 @@ def q4_weight_grad(dy: Q4Matrix, x: Q4Matrix, out=None, dtype=None, base=None,
     ``muon_step``) or a new tensor of ``dtype`` (``base``'s, or bf16).  ``base``
     has the result's dtype and may be ``out`` itself, which adds to the gradient
     in place."""
-    codes, scales, rows, tokens, at = _form_of(dy, True, "dy")
-    x_codes, x_scales, outs, x_tokens, x_at = _form_of(x, True, "x")
+    codes, scales, rows, tokens, p, ps = _form_of(dy, True, "dy")
+    x_codes, x_scales, outs, x_tokens, x_p, x_ps = _form_of(x, True, "x")
     device = codes.device
     if stream is not None:
         _check_stream(device, stream)
@@ -341,13 +340,13 @@ def q4_weight_grad(dy: Q4Matrix, x: Q4Matrix, out=None, dtype=None, base=None,
         _check_tensor(base, "base", (rows, outs), out.dtype, device)
     dt = _dtype_code(out)
     lib = load()
-    if at is None:
-        codes, scales, at = _dense_form(codes, scales, stream)
-    if x_at is None:
-        x_codes, x_scales, x_at = _dense_form(x_codes, x_scales, stream)
+    if p is None:
+        codes, scales, p, ps = _dense_form(codes, scales, stream)
+    if x_p is None:
+        x_codes, x_scales, x_p, x_ps = _dense_form(x_codes, x_scales, stream)
     ws, nws, keep = _scratch(_workspace_bytes("dmuon_q4_matmul", rows, outs, tokens), workspace, device, stream)
     if stream is not None:
         _keep(device, stream, (out,), made, (codes, scales, x_codes, x_scales, base))
-    _run(lib.dmuon_q4_matmul, device, stream, *at, rows, *x_at, outs, tokens,
+    _run(lib.dmuon_q4_matmul, device, stream, p, ps, rows, x_p, x_ps, outs, tokens,
          base.data_ptr() if base is not None else None, out.data_ptr(), dt, ws, nws)
     return out
