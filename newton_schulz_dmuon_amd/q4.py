@@ -39,7 +39,8 @@ from typing import List, Optional, Sequence
 from . import _lib
 from ._lib import DmuonError, Q4SourceDesc, check, load
 from .api import Workspace, _allocating, _dtype_code, _mark_used, _ptr
-from .q8 import _check_stream, _check_tensor, _check_untracked, _invalid, _keep, _matrix, _run, _scratch, _up
+from .q8 import (_check_no_tangent, _check_stream, _check_tensor, _check_untracked, _invalid, _keep, _matrix, _run,
+                 _scratch, _up)
 
 BLOCK = 32
 PAD = 256
@@ -204,7 +205,9 @@ def q4_quantize_weights(params: Sequence, out: Optional[Sequence[Q4Matrix]] = No
     if n == 0:
         return []
     for i, p in enumerate(params):
-        if not p.is_leaf:  # a parameter may be quantised, as the step may update it
+        if p.is_leaf:  # a parameter may be quantised, as the step may update it
+            _check_no_tangent(p, f"matrix {i}")
+        else:
             _check_untracked(p, f"matrix {i}")
     device = params[0].device
     for i, p in enumerate(params):

@@ -19,16 +19,16 @@ A training step of one linear layer::
 The functions enqueue kernels on ``stream`` (the current one by default) and
 record no gradients: the backward pass is the last two calls.  An input that
 requires one is refused while gradients are recorded (parameters that
-``q8_quantize_weights`` reads excepted).  Results that are
-not passed in are new tensors; without ``workspace`` a call that needs scratch
-allocates it.  On a ``stream`` of its own a call's results and scratch belong to
-that stream, and all its tensors may be dropped as soon as it returns; the caller
-only orders the streams (``stream`` after the work that makes the inputs, the
-readers of the results after ``stream``).  A ``Workspace`` serves
-any number of calls on one stream; work that may overlap (calls on two streams, a
-call and a replayed graph, two graphs) needs one each, and a graph's has to live
-as long as the graph.  Every call can be captured into a graph, and the same call
-gives the same bits.
+``q8_quantize_weights`` reads excepted), and so is one with a tangent of
+forward-mode differentiation.  Results that are not passed in are new tensors;
+without ``workspace`` a call that needs scratch allocates it.  On a ``stream`` of
+its own a call's results and scratch belong to that stream, and all its tensors may
+be dropped as soon as it returns; the caller only orders the streams (``stream``
+after the work that makes the inputs, the readers of the results after
+``stream``).  A ``Workspace`` serves any number of calls on one stream; work that
+may overlap (calls on two streams, a call and a replayed graph, two graphs) needs
+one each, and a graph's has to live as long as the graph.  Every call can be
+captured into a graph, and the same call gives the same bits.
 """
 
 from __future__ import annotations
@@ -119,9 +119,27 @@ def _check_rows(q: Q8Rows, rows: int) -> None:
     _check_tensor(q.scales, "scales", (kp // BLOCK, _up(rows, 4)), torch.uint8, q.codes.device)
 
 
+_forward_ad = None
+
+
+def _check_no_tangent(t, what: str) -> None:
+    """The same of forward-mode differentiation, whose tensors require no gradient
+    and which torch.no_grad() does not switch off."""
+    global _forward_ad
+    if _forward_ad is None:
+        from torch.autograd import forward_ad
+        _forward_ad = forward_ad
+    # without an open level no tensor has a tangent (nor is it looked for, half a
+    # microsecond a tensor)
+    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+        raise _invalid(f"{what} has a tangent, which this call does not carry on; call it in an "
+                       "autograd.Function or on a detached tensor")
+
+
 def _check_untracked(t, what: str) -> None:
     """No result carries a gradient on: an input that autograd tracks would leave
     its graph without a word."""
+    _check_no_tangent(t, what)
     if not t.requires_grad:
         return
     import torch
@@ -208,7 +226,9 @@ def q8_quantize_weights(params: Sequence, out: Optional[Sequence[Q8Weight]] = No
     if n == 0:
         return []
     for i, p in enumerate(params):
-        if not p.is_leaf:  # a parameter may be quantised, as the step may update it
+        if p.is_leaf:  # a parameter may be quantised, as the step may update it
+            _check_no_tangent(p, f"matrix {i}")
+        else:
             _check_untracked(p, f"matrix {i}")
     device = params[0].device
     for i, p in enumerate(params):
