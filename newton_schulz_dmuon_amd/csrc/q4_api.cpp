@@ -235,4 +235,17 @@ int dmuon_q4_rows_matmul(const void *x, int64_t rows, const void *codes_b, const
   });
 }
 
+// Not part of the public ABI: the tests ask it which kernels their sizes run in.
+// choice: Q4Choice's first four numbers, then ta, tb, whole, tail, pieces.
+int dmuon_q4_choice(int32_t bf16_rows, int64_t rows, int64_t outs, int64_t inner, int64_t *choice) {
+  return guarded([&]() -> int {
+    const int rc = check_sizes(rows, outs, inner, 1);
+    if (rc) return rc;
+    const Q4Choice c = bf16_rows ? q4_rows_choice(rows, outs, inner) : q4_matmul_choice(rows, outs, round_up(inner, kQ4Pad));
+    const int64_t out[] = {c.row_blocks, c.out_blocks, c.waves, c.rows, c.tiles.ta, c.tiles.tb, c.tiles.whole, c.tiles.tail, c.tiles.pieces};
+    std::memcpy(choice, out, sizeof out);
+    return DMUON_OK;
+  });
+}
+
 }  // extern "C"

@@ -65,4 +65,13 @@ hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st);
 size_t q4_rows_workspace(int64_t rows, int64_t outs, int64_t inner);
 hipError_t launch_q4_rows(const Q4Product &p, hipStream_t st);
 
+// The kernel that a product of these sizes runs in: a streaming work-group's blocks of
+// 16 rows and outputs and the rows that it loads (blocks 0: in tiles), or the tiles.
+struct Q4Choice {
+  int32_t row_blocks, out_blocks, waves, rows;
+  TileSplit tiles;
+};
+Q4Choice q4_matmul_choice(int64_t rows, int64_t outs, int64_t kp);
+Q4Choice q4_rows_choice(int64_t rows, int64_t outs, int64_t inner);
+
 }  // namespace dmuon

@@ -690,6 +690,11 @@ hipError_t launch_stream(const Q4Product &p, hipStream_t st) {
 
 size_t q4_matmul_workspace(int64_t rows, int64_t outs, int64_t kp) { return plan_of(rows, outs, kp).split.ws_bytes(); }
 
+Q4Choice q4_matmul_choice(int64_t rows, int64_t outs, int64_t kp) {
+  const Plan pl = plan_of(rows, outs, kp);
+  return Q4Choice{pl.nt, pl.nn, pl.waves, pl.nt == 0 ? 0 : pl.nt > 1 || rows > 8 ? 16 : 8, pl.split};
+}
+
 hipError_t launch_q4_matmul(const Q4Product &p, hipStream_t st) {
   if (p.kp == 0) {
     const int64_t groups = std::min<int64_t>((p.rows * p.outs + 2047) / 2048, 1 << 20);

@@ -681,6 +681,12 @@ size_t q4_rows_workspace(int64_t rows, int64_t outs, int64_t inner) {
   return pl.pad_bytes + pl.piece_bytes;
 }
 
+Q4Choice q4_rows_choice(int64_t rows, int64_t outs, int64_t inner) {
+  const Plan pl = plan_of(rows, outs, inner);
+  if (pl.nn == 0) return Q4Choice{0, 0, 0, 0, pl.split};
+  return Q4Choice{1, pl.nn, kStreamWaves, static_cast<int32_t>(stream_rows(rows)), pl.split};
+}
+
 hipError_t launch_q4_rows(const Q4Product &args, hipStream_t st) {
   Q4Product p = args;
   const Plan pl = plan_of(p.rows, p.outs, p.inner);
