@@ -213,8 +213,8 @@ def workspace_bytes(params, opts: StepOptions) -> int:
 
 
 class Workspace:
-    """Device scratch for ``muon_step`` and the 8-bit products, grown on demand
-    (PyTorch allocates).  Buffers that were used in a graph's capture are kept
+    """Device scratch for ``muon_step`` and the 8-bit and 4-bit products, grown on
+    demand (PyTorch allocates).  Buffers that were used in a graph's capture are kept
     when a larger call replaces them, since the graph's replays write them; a
     Workspace has to live as long as the graphs captured with it."""
 

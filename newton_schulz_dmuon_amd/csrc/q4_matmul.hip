@@ -228,12 +228,16 @@ __global__ __launch_bounds__(WAVES * 64) void q4_stream_kernel(Q4Product p) {
 // read fragments and issue the next stage's loads while the other half's multiply,
 // switching at every barrier.
 //
-// Bound by the power that the matrix instructions draw: 256 x 256 takes 1.28 us a step
-// on zero codes and 1.65 to 1.9 on random ones, where a loop of nothing else reaches
-// 7.1 PFLOP/s on random codes and 9.6 on zeros.  8192 rows by 14336 x 4096: 239 us, 4.0
-// PFLOP/s (a library product of the same type 350), of which the stores are 13%.  With
-// four waves of 128 x 128 it took 293 us for 290, with the next tile's first loads sent
-// before the stores 296 for 295: neither was kept.
+// 8192 rows by 14336 x 4096: 239 us, 4.0 PFLOP/s (a library product of the same type
+// 350).  Not bound by the matrix instructions, which are busy 45% of the cycles: they
+// alone, their operands left in registers, take 145 us, everything else without them
+// 152, without the loads 164, without the stores 205.  So the loads into LDS beside the
+// instructions and fragment reads cost 75 us, and the stores, beside which nothing runs,
+// 34.  The power that the instructions draw takes some of the clock: on zero codes the
+// whole takes 190 us, the instructions alone 117 (a loop of nothing else reaches 7.1
+// PFLOP/s on random codes and 9.6 on zeros).  With four waves of 128 x 128 it took 293
+// us for 290, with the next tile's first loads sent before the stores 296 for 295:
+// neither was kept.
 //
 // The order of rows in LDS is free, since every lane of a load picks its global
 // row, and is chosen for the ends of the pipeline: a wave's block i, row q holds

@@ -193,16 +193,21 @@ __global__ __launch_bounds__(kStreamWaves * 64) void q4_rows_stream_kernel(Q4Pro
 // by 256 rows, TB below; each wave TA/2 x TB/4 in 16 x 16 blocks.  K advances 64 elements per step: 128
 // bytes of a row, and a quarter of the 256 codes (128 bytes) that a stage of the
 // weight holds.  Both come into LDS by LDS-bound loads (16 bytes a lane, 128-byte
-// rows, the 16-byte chunk XORed with (row / 2) mod 8, which keeps the fragment reads
-// off each other's banks), in a ring of two stages each: a step loads the next
-// step's rows and a quarter of the next stage of the weight.  The two halves of the
-// work-group (wm) run in ping-pong: one half's waves read fragments and issue loads
-// while the other half's expand and multiply, switching at every barrier.
+// rows, the 16-byte chunk XORed with (row / 2) mod 8), in a ring of two stages each: a
+// step loads the next step's rows and a quarter of the next stage of the weight.  The
+// XOR is the 4-bit product's, where it keeps the fragment reads off each other's banks;
+// here, where a lane reads chunks 2 g4 and 2 g4 + 1 of a row, half of the cycles in
+// which LDS is active (30% of all) are conflicts.  The two halves of the work-group
+// (wm) run in ping-pong: one half's waves read fragments and issue loads while the
+// other half's expand and multiply, switching at every barrier.
 //
-// Bound by the matrix instructions at the clock that their power leaves: 2048 rows by
-// 14336 x 4096 176 to 180 us, 1.34 to 1.37 PFLOP/s, a large library product's rate
-// (1.36).  Expansions placed between the matrix instructions by hand changed nothing
-// (128 x 256: 65 -> 70 us of 2048 rows by 4096 x 4096).
+// 2048 rows by 14336 x 4096 take 175 to 180 us, 1.34 to 1.37 PFLOP/s, a large library
+// product's rate (1.36).  The matrix instructions, busy 54% of the cycles, and the
+// expansions alone, their operands left in registers, take 123 us, everything else
+// without them 134, without the loads 158, without the stores 169: neither hides the
+// other.  On zeros the whole takes 169, so the clock that power leaves is little of it.
+// Expansions placed between the matrix instructions by hand were slower (128 x 256: 65
+// -> 70 us of 2048 rows by 4096 x 4096).
 //
 // A lane's 16 codes of a step are k = 16 g4 + 0 .. 15, eight of them an instruction.
 // The order of rows in LDS is that of the 4-bit product's tiles.
