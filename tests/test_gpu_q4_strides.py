@@ -125,3 +125,22 @@ def test_results_must_be_contiguous():
             nsd.q4_quantize(rows, out=q)
         with pytest.raises(nsd.DmuonError, match="contiguous"):
             nsd.q4_quantize_weights([rows], out=[q])
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes of transposed codes, read where they lie first and last."""
+    rows, cols = (1 << 21) + 5, 4100
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough memory")
+    print("offsets beyond 32 bits", flush=True)
+    torch.manual_seed(3)
+    raw = torch.randint(0, 256, (2176, rows), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(100, 150, (136, (rows + 15) // 16 * 16), dtype=torch.uint8, device="cuda")
+    got = nsd.q4_dequantize(nsd.Q4Matrix(rows, cols, raw.t(), scales))
+    for lo, hi in ((0, 300), (rows // 2, rows // 2 + 300), (rows - 300, rows)):
+        s = scales[:, lo:hi]
+        s = torch.nn.functional.pad(s, (0, -s.shape[1] % 16), value=2).contiguous()
+        want = nsd.q4_dequantize(nsd.Q4Matrix(hi - lo, cols, raw[:, lo:hi].t().contiguous(), s))
+        assert torch.equal(got[lo:hi], want)
+    del got, raw
+    torch.cuda.empty_cache()
