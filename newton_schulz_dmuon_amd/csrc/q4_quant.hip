@@ -175,9 +175,12 @@ __device__ __forceinline__ uint32_t codes8(const Pairs<F32> &x, int byte, N n) {
 
 // Eight bytes from `at` on, of eight rows `step` apart.  Loads at any byte's address
 // are slow (8192 x 4095 elements 61 us): whole words are loaded and shifted, where
-// none of them lies behind the `size` bytes.
+// none of a wave's lies behind the `size` bytes.  The branch is the wave's: where each
+// lane took its own, the built code lost the elements that lanes of the first side
+// had loaded before.
 __device__ __forceinline__ void load_bytes(const uint8_t *p, int64_t at, int64_t step, int64_t size, u32x2 (&n)[8]) {
-  if ((step & 7) == 0 || at + 7 * step + 12 > size) {
+  const bool behind = at + 7 * step + 12 > size;
+  if (((step & 7) == 0) | (__builtin_amdgcn_ballot_w64(behind) != 0)) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) n[r] = *(const g_u32x2_at1 *)(p + at + r * step);
     return;
